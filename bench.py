@@ -81,11 +81,11 @@ def measured_traffic(workload: str, op: str):
     cap = MEASURED_TRAFFIC.get("csrc_digest")
     if cap is None:
         return None, "no ncu capture recorded for the current kernels"
-    if cap != csrc_digest():
-        return None, f"stale: the CUDA sources changed since the ncu capture ({cap})"
     v = MEASURED_TRAFFIC.get(workload, {}).get(op)
     if v is None:
         return None, f"no ncu capture of this kernel at {workload}"
+    if cap != csrc_digest():
+        return None, f"stale: the CUDA sources changed since the ncu capture ({cap})"
     return v, f"ncu capture of sources {cap}"
 
 
