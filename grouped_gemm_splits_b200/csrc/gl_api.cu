@@ -1,5 +1,7 @@
 // gl_api.cu -- the C ABI (include/gl.h): argument checks, then launches.
 // Nothing here allocates device memory or synchronises the host.
+#include <algorithm>
+
 #include "gl_internal.h"
 
 namespace {
@@ -423,6 +425,64 @@ size_t gl_mxfp8_scale_bytes(int64_t rows, int cols, int G, int colwise, int scal
   if (scale_layout == GL_SCALES_ROWMAJOR) return colwise ? ((r + 31) / 32 + g) * c : r * (c / 32);
   if (scale_layout != GL_SCALES_MMA || cols % 128 != 0) return 0;
   return (colwise ? (r + 127) / 128 + g : (r + 127) / 128) * (c / 128) * 512;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- RMS norm
+namespace {
+
+gl_status check_norm_dims(int64_t rows, int cols) {
+  if (rows < 0 || cols <= 0) return GL_ERR_INVALID;
+  if (cols % 8 != 0 || cols > GL_NORM_MAX_COLS) return GL_ERR_UNSUPPORTED;
+  if (rows >= (int64_t(1) << 31)) return GL_ERR_UNSUPPORTED;
+  return GL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gl_status gl_rmsnorm(const void* x, const void* residual, const void* gamma, float eps, int64_t rows, int cols,
+                     void* sum, void* y, float* rstd, uint8_t* codes, uint8_t* scales, int scale_layout,
+                     void* stream) {
+  const gl_status st = check_norm_dims(rows, cols);
+  if (st != GL_OK) return st;
+  if (!(eps >= 0.0f) || gamma == nullptr) return GL_ERR_INVALID;
+  if (scale_layout != GL_SCALES_ROWMAJOR && scale_layout != GL_SCALES_MMA) return GL_ERR_INVALID;
+  if (rows > 0) {
+    if (x == nullptr || (y == nullptr && codes == nullptr)) return GL_ERR_INVALID;
+    if (codes != nullptr && scales == nullptr) return GL_ERR_INVALID;
+    if (sum != nullptr && sum == y) return GL_ERR_INVALID;
+  }
+  if (codes != nullptr && (cols % 32 != 0 || (scale_layout == GL_SCALES_MMA && cols % 128 != 0)))
+    return GL_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(sum) || !aligned16(y) ||
+      (reinterpret_cast<uintptr_t>(rstd) & 3u) || (reinterpret_cast<uintptr_t>(codes) & 7u))
+    return GL_ERR_UNSUPPORTED;
+  if (rows == 0) return GL_OK;
+  return gl::launch_rmsnorm(x, residual, gamma, eps, rows, cols, sum, y, rstd, codes, scales, scale_layout,
+                            to_stream(stream));
+}
+
+size_t gl_rmsnorm_bwd_workspace_bytes(int64_t rows, int cols) {
+  if (check_norm_dims(rows, cols) != GL_OK) return 0;
+  return static_cast<size_t>(std::max<int64_t>(gl::rmsnorm_bwd_blocks(rows, cols), 1)) * cols * 4;
+}
+
+gl_status gl_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma, const float* rstd, const void* dsum,
+                         int64_t rows, int cols, void* dx, float* dgamma, int accumulate, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const gl_status st = check_norm_dims(rows, cols);
+  if (st != GL_OK) return st;
+  if (gamma == nullptr || dgamma == nullptr || workspace == nullptr) return GL_ERR_INVALID;
+  if (rows > 0 && (dy == nullptr || sum == nullptr || rstd == nullptr || dx == nullptr)) return GL_ERR_INVALID;
+  if (workspace_bytes < gl_rmsnorm_bwd_workspace_bytes(rows, cols)) return GL_ERR_INVALID;
+  if (!aligned16(dy) || !aligned16(sum) || !aligned16(gamma) || !aligned16(dsum) || !aligned16(dx) ||
+      !aligned16(dgamma) || (reinterpret_cast<uintptr_t>(rstd) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return GL_ERR_UNSUPPORTED;
+  return gl::launch_rmsnorm_bwd(dy, sum, gamma, rstd, dsum, rows, cols, dx, dgamma, accumulate ? 1 : 0,
+                                static_cast<float*>(workspace), to_stream(stream));
 }
 
 }  // extern "C"

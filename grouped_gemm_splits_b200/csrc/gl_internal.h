@@ -101,4 +101,14 @@ gl_status check_quantize_dbias_args(const void* src, int64_t rows, int cols, con
 gl_status launch_dbias_partials(const float* part, const int64_t* part_prefix, int32_t* status, int G, int N,
                                 gl_grouped dbias, cudaStream_t stream);
 
+// RMS norm (gl_norm.cu).  The backward pass writes one row of cols partial
+// dgamma sums per block into `part`.
+gl_status launch_rmsnorm(const void* x, const void* residual, const void* gamma, float eps, int64_t rows, int cols,
+                         void* sum, void* y, float* rstd, uint8_t* codes, uint8_t* scales, int scale_layout,
+                         cudaStream_t stream);
+int64_t rmsnorm_bwd_blocks(int64_t rows, int cols);
+gl_status launch_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma, const float* rstd, const void* dsum,
+                             int64_t rows, int cols, void* dx, float* dgamma, int accumulate, float* part,
+                             cudaStream_t stream);
+
 }  // namespace gl

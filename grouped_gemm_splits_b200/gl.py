@@ -25,7 +25,8 @@ GL_SCALES_ROWMAJOR, GL_SCALES_MMA = 0, 1
 
 EXPORTED = ("gl_version", "gl_status_string", "gl_offsets", "gl_fwd", "gl_dgrad", "gl_wgrad",
             "gl_dbias", "group_quantize_mxfp8", "gl_mxfp8_scale_bytes", "gl_dbias_workspace_bytes",
-            "group_quantize_mxfp8_dbias", "gl_fwd_mxfp8", "gl_dgrad_mxfp8", "gl_wgrad_mxfp8")
+            "group_quantize_mxfp8_dbias", "gl_fwd_mxfp8", "gl_dgrad_mxfp8", "gl_wgrad_mxfp8",
+            "gl_rmsnorm", "gl_rmsnorm_bwd", "gl_rmsnorm_bwd_workspace_bytes")
 
 
 class GlGrouped(ctypes.Structure):
@@ -90,6 +91,12 @@ def load() -> ctypes.CDLL:
     L.gl_dgrad_mxfp8.argtypes = [vp, vp, GlGrouped, GlGrouped, vp, vp, i32, i64, i32, i32, vp, i64, op, vp]
     L.gl_wgrad_mxfp8.restype = i32
     L.gl_wgrad_mxfp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, GlGrouped, i32, op, vp]
+    L.gl_rmsnorm.restype = i32
+    L.gl_rmsnorm.argtypes = [vp, vp, vp, ctypes.c_float, i64, i32, vp, vp, vp, vp, vp, i32, vp]
+    L.gl_rmsnorm_bwd.restype = i32
+    L.gl_rmsnorm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, vp, i32, vp, ctypes.c_size_t, vp]
+    L.gl_rmsnorm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    L.gl_rmsnorm_bwd_workspace_bytes.argtypes = [i64, i32]
     _lib = L
     return L
 
@@ -386,3 +393,136 @@ def gl_wgrad_mxfp8(x_codes_c: torch.Tensor, x_scales_c: torch.Tensor, dy_codes_c
                                  1 if accumulate else 0, _opts(pair, wait_limit_us, opt_flags), _stream()), "gl_wgrad_mxfp8")
     del keep
     return main_grad
+
+
+# ------------------------------------------------------------------- RMS norm
+
+def _need(ok: bool, what: str, why: str) -> None:
+    if not ok:
+        raise GlError(f"{what}: {why}")
+
+
+def _tensor(what: str, name: str, t, dtype, *shapes) -> None:
+    """Refuse anything but a contiguous tensor of this dtype and one of these shapes."""
+    _need(isinstance(t, torch.Tensor), what, f"{name} must be a tensor")
+    _need(t.dtype == dtype, what, f"{name} must be {dtype}, not {t.dtype}")
+    _need(tuple(t.shape) in shapes, what, f"{name} must be {' or '.join(map(str, shapes))}, not {tuple(t.shape)}")
+    _need(t.is_contiguous(), what, f"{name} must be contiguous")
+
+
+class _On:
+    """The device of a call's tensors, made current for the call; yields its current stream."""
+
+    def __init__(self, what: str, *tensors):
+        dev = tensors[0].device
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise GlError(f"{what}: tensors on {dev} and {t.device}")
+        _need(dev.type == "cuda", what, f"tensors must be on a CUDA device, not {dev}")
+        self.dev = dev
+
+    def __enter__(self):
+        self.old = torch.cuda.current_device()
+        if self.old != self.dev.index:
+            torch.cuda.set_device(self.dev)
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.old != self.dev.index:
+            torch.cuda.set_device(self.old)
+
+
+def gl_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+               y: bool = True, mxfp8: bool = False, mma_scales: bool = False, out: Optional[dict] = None) -> dict:
+    """RMS norm of ``x`` (+ ``residual``), bf16 [rows, cols].
+
+    Returns a dict: ``rstd`` (fp32 [rows]); ``sum`` (bf16, the new residual
+    stream) where there is a residual; ``y`` (bf16) if asked for; with
+    ``mxfp8`` the rowwise ``codes_r`` / ``scales_r`` of the fp32 result, as
+    :func:`group_quantize_mxfp8` lays them out (``mma_scales``: the layout the
+    MXFP8 products read).  Tensors given in ``out`` are written instead of new
+    ones; ``out["sum"]`` and ``out["y"]`` may be ``x`` or ``residual``.
+    """
+    what = "gl_rmsnorm"
+    bf = torch.bfloat16
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2, what, "x must be a [rows, cols] tensor")
+    rows, cols = x.shape
+    _tensor(what, "x", x, bf, (rows, cols))
+    _tensor(what, "gamma", gamma, bf, (cols,))
+    if residual is not None:
+        _tensor(what, "residual", residual, bf, (rows, cols))
+    _need(y or mxfp8, what, "at least one of y and mxfp8 is required")
+    if mxfp8:
+        _need(cols % (128 if mma_scales else 32) == 0, what, f"cols = {cols} does not fit the scale layout")
+    out = {} if out is None else dict(out)
+    want = {"rstd": (torch.float32, (rows,))}
+    if residual is not None or "sum" in out:
+        want["sum"] = (bf, (rows, cols))
+    if y:
+        want["y"] = (bf, (rows, cols))
+    if mxfp8:
+        want["codes_r"] = (torch.uint8, (rows, cols))
+        want["scales_r"] = (torch.uint8, ((mxfp8_scale_bytes(rows, cols, 1, False, True) if rows else 0,)
+                                          if mma_scales else (rows, cols // 32)))
+    for key, t in out.items():
+        _need(key in want, what, f"out[{key!r}] is not an output of this call")
+        dt, shape = want[key]
+        if key == "scales_r":
+            _tensor(what, key, t, dt, shape, (rows * (cols // 32),) if not mma_scales else shape)
+        else:
+            _tensor(what, key, t, dt, shape)
+    with _On(what, x, gamma, residual, *out.values()) as stream:
+        for key, (dt, shape) in want.items():
+            if key not in out:
+                out[key] = torch.empty(shape, dtype=dt, device=x.device)
+        _check(load().gl_rmsnorm(x.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, rows, cols,
+                                 _ptr(out.get("sum")), _ptr(out.get("y")), out["rstd"].data_ptr(),
+                                 _ptr(out.get("codes_r")), _ptr(out.get("scales_r")),
+                                 GL_SCALES_MMA if mma_scales else GL_SCALES_ROWMAJOR, stream), what)
+    return out
+
+
+def rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    """Workspace bytes of :func:`gl_rmsnorm_bwd` on the current device."""
+    n = load().gl_rmsnorm_bwd_workspace_bytes(rows, cols)
+    if n == 0:
+        raise GlError(f"gl_rmsnorm_bwd_workspace_bytes: invalid arguments ({rows}, {cols})")
+    return n
+
+
+def gl_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor,
+                   dsum: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                   dgamma: Optional[torch.Tensor] = None, accumulate: bool = False,
+                   workspace: Optional[torch.Tensor] = None):
+    """Gradients of :func:`gl_rmsnorm`: (dx bf16 [rows, cols], dgamma fp32 [cols]).
+
+    ``dx`` is the gradient of x and of the residual alike; ``dsum`` is what
+    reaches the sum along the residual stream.  ``accumulate`` adds to the
+    given ``dgamma``.
+    """
+    what = "gl_rmsnorm_bwd"
+    bf = torch.bfloat16
+    _need(isinstance(dy, torch.Tensor) and dy.dim() == 2, what, "dy must be a [rows, cols] tensor")
+    rows, cols = dy.shape
+    _tensor(what, "dy", dy, bf, (rows, cols))
+    _tensor(what, "sum", sum, bf, (rows, cols))
+    _tensor(what, "gamma", gamma, bf, (cols,))
+    _tensor(what, "rstd", rstd, torch.float32, (rows,))
+    if dsum is not None:
+        _tensor(what, "dsum", dsum, bf, (rows, cols))
+    if dx is not None:
+        _tensor(what, "dx", dx, bf, (rows, cols))
+    if dgamma is not None:
+        _tensor(what, "dgamma", dgamma, torch.float32, (cols,))
+    _need(dgamma is not None or not accumulate, what, "accumulate needs a dgamma")
+    with _On(what, dy, sum, gamma, rstd, dsum, dx, dgamma, workspace) as stream:
+        if dx is None:
+            dx = torch.empty(rows, cols, dtype=bf, device=dy.device)
+        if dgamma is None:
+            dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
+        if workspace is None:
+            workspace = torch.empty(rmsnorm_bwd_workspace_bytes(rows, cols), dtype=torch.uint8, device=dy.device)
+        _check(load().gl_rmsnorm_bwd(dy.data_ptr(), sum.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), _ptr(dsum),
+                                     rows, cols, dx.data_ptr(), dgamma.data_ptr(), 1 if accumulate else 0,
+                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream), what)
+    return dx, dgamma

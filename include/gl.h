@@ -388,6 +388,74 @@ gl_status gl_wgrad_mxfp8(const uint8_t* x_codes_c, const uint8_t* x_scales_c, co
                          const uint8_t* dy_scales_c, const int64_t* offsets, int32_t* status, int G,
                          int64_t M, int N, int K, gl_grouped main_grad, int accumulate, const gl_gemm_opts* opts, void* stream);
 
+/*
+ * gl_rmsnorm -- root-mean-square norm of the rows of a residual stream, with
+ * the residual's addition before it and bf16 and / or MXFP8 output: the norm
+ * in front of a grouped linear layer, its MXFP8 form being the x operand of
+ * gl_fwd_mxfp8 as it is.  Per row, in fp32 from the bf16 inputs:
+ *     s = x + residual
+ *     rstd = 1 / sqrt(sum(s^2) / cols + eps)
+ *     y = s * rstd * gamma
+ * Every output is rounded once: the norm is taken of the fp32 sum, and the
+ * codes come from the fp32 y (so a code may differ by one step from a cast of
+ * the bf16 y).
+ *
+ *   x         device bf16 [rows, cols]
+ *   residual  NULL (s = x) or device bf16 [rows, cols]
+ *   gamma     device bf16 [cols]
+ *   sum       NULL or device bf16 [rows, cols], written: s, the new residual
+ *             stream (and what gl_rmsnorm_bwd reads)
+ *   y         NULL or device bf16 [rows, cols], written
+ *   rstd      NULL or device fp32 [rows], written
+ *   codes     NULL or device u8 [rows, cols], written: rowwise E4M3 codes of y
+ *   scales    device u8 (required with codes) of gl_mxfp8_scale_bytes(rows,
+ *             cols, 1, 0, scale_layout) bytes: E8M0 scales as
+ *             group_quantize_mxfp8 writes them
+ * At least one of y and codes is required.  sum and y may each be the same
+ * buffer as x or residual (in place), not the same as each other; otherwise
+ * buffers do not overlap.
+ * Limits: cols % 8 == 0 (16-byte rows), cols % 32 == 0 with codes,
+ * cols % 128 == 0 with GL_SCALES_MMA, cols <= GL_NORM_MAX_COLS; pointers
+ * 16-byte aligned (codes 8, scales and rstd by their element).  The squares
+ * of a row must not overflow fp32 (|s| below 2^60 suffices); a row that holds
+ * a NaN or an infinity gives NaN where the formula does.  rows == 0 does nothing.
+ */
+#define GL_NORM_MAX_COLS 16384
+gl_status gl_rmsnorm(const void* x, const void* residual, const void* gamma, float eps, int64_t rows,
+                     int cols, void* sum, void* y, float* rstd, uint8_t* codes, uint8_t* scales,
+                     int scale_layout, void* stream);
+
+/*
+ * gl_rmsnorm_bwd -- gradients of gl_rmsnorm.  With xh = s * rstd, g = dy * gamma:
+ *     dx = rstd * (g - xh * mean over the row of g * xh) (+ dsum)
+ *     dgamma[c] (+)= sum over the rows of dy * xh
+ * dx is the gradient of x and of residual alike (both enter by their sum);
+ * dsum is the gradient that reaches s past the norm, along the residual
+ * stream.  The row sums are added in a fixed order: results are deterministic
+ * for a given GPU.
+ *
+ *   dy, sum    device bf16 [rows, cols]; sum as gl_rmsnorm wrote it (x itself
+ *              where there was no residual)
+ *   gamma      device bf16 [cols]
+ *   rstd       device fp32 [rows] from gl_rmsnorm
+ *   dsum       NULL or device bf16 [rows, cols]
+ *   dx         device bf16 [rows, cols], written; may be the same buffer as
+ *              dy or dsum
+ *   dgamma     device fp32 [cols]: accumulate != 0 adds to it, 0 overwrites
+ *   workspace  device scratch of workspace_bytes >=
+ *              gl_rmsnorm_bwd_workspace_bytes(rows, cols), 256-byte aligned;
+ *              its contents on entry do not matter
+ * The size of the workspace follows the current device's SM count.  Limits
+ * as for gl_rmsnorm; two launches.  rows == 0 writes zeros to dgamma when it
+ * overwrites.
+ */
+gl_status gl_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma, const float* rstd,
+                         const void* dsum, int64_t rows, int cols, void* dx, float* dgamma, int accumulate,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes for gl_rmsnorm_bwd; 0 for invalid arguments. */
+size_t gl_rmsnorm_bwd_workspace_bytes(int64_t rows, int cols);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,50 @@
+"""The block oracle (norm, activations, few-token layer) against torch autograd
+in 64 bits, differences, and values worked by hand."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_oracle as blk
+
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_rmsnorm_is_the_autograd_of_its_formula(residual):
+    rng = np.random.default_rng(5)
+    x, r, dy, ds = (torch.tensor(rng.standard_normal((7, 40)), requires_grad=True) for _ in range(4))
+    gamma = torch.tensor(rng.standard_normal(40), requires_grad=True)
+    s = x + r if residual else x
+    y = s / torch.sqrt((s * s).mean(1, keepdim=True) + 1e-3) * gamma
+    (y * dy.detach() + s * ds.detach()).sum().backward()
+    n = [t.detach().numpy() for t in (x, r, gamma, dy, ds)]
+    s64, rstd, y64 = blk.rmsnorm(n[0], n[1] if residual else None, n[2], 1e-3)
+    np.testing.assert_allclose(y64, y.detach().numpy(), rtol=1e-12)
+    np.testing.assert_allclose(s64, s.detach().numpy(), rtol=1e-12)
+    dx, dgamma = blk.rmsnorm_bwd(n[3], s64, n[2], rstd, n[4])
+    np.testing.assert_allclose(dx, x.grad.numpy(), rtol=1e-9, atol=1e-12)
+    np.testing.assert_allclose(dgamma, gamma.grad.numpy(), rtol=1e-9, atol=1e-12)
+    if residual:
+        np.testing.assert_allclose(dx, r.grad.numpy(), rtol=1e-9, atol=1e-12)
+
+
+def test_rmsnorm_gradient_against_differences():
+    rng = np.random.default_rng(6)
+    x, dy = rng.standard_normal((3, 16)), rng.standard_normal((3, 16))
+    gamma = rng.standard_normal(16)
+
+    def loss(x, gamma):
+        return float(np.sum(blk.rmsnorm(x, None, gamma, 1e-5)[2] * dy))
+
+    s, rstd, _ = blk.rmsnorm(x, None, gamma, 1e-5)
+    dx, dgamma = blk.rmsnorm_bwd(dy, s, gamma, rstd, None)
+    h = 1e-6
+    for i, j in ((0, 0), (1, 7), (2, 15)):
+        e = np.zeros_like(x)
+        e[i, j] = h
+        assert abs((loss(x + e, gamma) - loss(x - e, gamma)) / (2 * h) - dx[i, j]) < 1e-7
+        assert abs((loss(x, gamma + e[i]) - loss(x, gamma - e[i])) / (2 * h) - dgamma[j]) < 1e-7
+
+
+def test_rmsnorm_by_hand():
+    s, rstd, y = blk.rmsnorm(np.array([[3.0, 4.0]]), np.array([[0.0, 0.0]]), np.array([1.0, 2.0]), 0.0)
+    assert rstd[0] == pytest.approx(1 / np.sqrt(12.5))
+    np.testing.assert_allclose(y, [[3 / np.sqrt(12.5), 8 / np.sqrt(12.5)]])
