@@ -2,6 +2,7 @@
 // Nothing here allocates device memory or synchronises the host.
 #include <algorithm>
 
+#include "gl_act.cuh"
 #include "gl_internal.h"
 
 namespace {
@@ -184,6 +185,88 @@ gl_status gl_wgrad(const void* x, const void* dy, const int64_t* offsets, int32_
   c.wait_ns = wait_ns;
   c.hold_loads = hold;
   c.stream = to_stream(stream);
+  return gl::launch_grouped_gemm(c);
+}
+
+gl_status gl_fwd_act(const void* x, gl_grouped w, const gl_grouped* bias, const void* residual, int act,
+                     const int64_t* offsets, int32_t* status, int G, int64_t M, int N, int K, void* z, void* y,
+                     int64_t y_rows, const gl_gemm_opts* opts, void* stream) {
+  gl_status st = check_gemm_dims(G, M, N, K);
+  if (st != GL_OK) return st;
+  int pair = 1, hold = 0;
+  uint64_t wait_ns = 0;
+  if (!read_opts(opts, &pair, &wait_ns, &hold)) return GL_ERR_INVALID;
+  if (act < GL_ACT_NONE || act > GL_ACT_GEGLU) return GL_ERR_INVALID;
+  if ((x == nullptr && M > 0) || (y == nullptr && M > 0) || offsets == nullptr || status == nullptr)
+    return GL_ERR_INVALID;
+  if (!grouped_ok(w, G) || (bias != nullptr && !grouped_ok(*bias, G))) return GL_ERR_INVALID;
+  if (y_rows < M) return GL_ERR_INVALID;
+  if (M > 0 && z != nullptr && (z == y || z == residual)) return GL_ERR_INVALID;
+  if (gl::act_gated(act) && N % 16 != 0) return GL_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(z) || !aligned16(residual) || !grouped_aligned(w, G) ||
+      (bias && !grouped_aligned(*bias, G)))
+    return GL_ERR_UNSUPPORTED;
+  if (M == 0) return GL_OK;
+  GemmCall c{};
+  c.mode = gl::kFwd;
+  c.a = x;
+  c.w = w;
+  c.bias = bias;
+  c.out = y;
+  c.out_rows = y_rows;
+  c.offsets = offsets;
+  c.status = status;
+  c.G = G;
+  c.M = M;
+  c.N = N;
+  c.K = K;
+  c.cta_pair = pair;
+  c.wait_ns = wait_ns;
+  c.hold_loads = hold;
+  c.stream = to_stream(stream);
+  c.epilogue = 1;
+  c.act = act;
+  c.residual = residual;
+  c.z = z;
+  return gl::launch_grouped_gemm(c);
+}
+
+gl_status gl_dgrad_act(const void* dy, gl_grouped w, const void* z, int act, const int64_t* offsets, int32_t* status,
+                       int G, int64_t M, int N, int K, void* dz, int64_t dz_rows, const gl_gemm_opts* opts,
+                       void* stream) {
+  gl_status st = check_gemm_dims(G, M, N, K);
+  if (st != GL_OK) return st;
+  int pair = 1, hold = 0;
+  uint64_t wait_ns = 0;
+  if (!read_opts(opts, &pair, &wait_ns, &hold)) return GL_ERR_INVALID;
+  if (act <= GL_ACT_NONE || act > GL_ACT_GEGLU) return GL_ERR_INVALID;
+  if (((dy == nullptr || z == nullptr || dz == nullptr) && M > 0) || offsets == nullptr || status == nullptr)
+    return GL_ERR_INVALID;
+  if (!grouped_ok(w, G)) return GL_ERR_INVALID;
+  if (dz_rows < M) return GL_ERR_INVALID;
+  if (M > 0 && z == dz) return GL_ERR_INVALID;
+  if (gl::act_gated(act) && K > (1 << 30)) return GL_ERR_UNSUPPORTED;  // 2K columns of z
+  if (!aligned16(dy) || !aligned16(z) || !aligned16(dz) || !grouped_aligned(w, G)) return GL_ERR_UNSUPPORTED;
+  if (M == 0) return GL_OK;
+  GemmCall c{};
+  c.mode = gl::kDgrad;
+  c.a = dy;
+  c.w = w;
+  c.out = dz;
+  c.out_rows = dz_rows;
+  c.offsets = offsets;
+  c.status = status;
+  c.G = G;
+  c.M = M;
+  c.N = N;
+  c.K = K;
+  c.cta_pair = pair;
+  c.wait_ns = wait_ns;
+  c.hold_loads = hold;
+  c.stream = to_stream(stream);
+  c.epilogue = 1;
+  c.act = act;
+  c.z = const_cast<void*>(z);
   return gl::launch_grouped_gemm(c);
 }
 

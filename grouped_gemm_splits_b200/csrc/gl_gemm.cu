@@ -26,6 +26,20 @@
 // epilogue overlap the next tile's main loop.  Tiles are enumerated group by
 // group from the device offsets (tile prefix in shared memory): empty groups
 // cost nothing and the host never learns the split sizes.
+//
+// Epilogue forms (EPI) of FWD and DGRAD, gl_fwd_act / gl_dgrad_act:
+//
+//   kEpiAct    y = act(u) (+ r), u = x W^T (+ b);        dz = (dy W) act'(z)
+//   kEpiGated  y = act(u0) u1 (+ r), u0 | u1 = halves of u;
+//              dz0 | dz1 = (dy W) z1 act'(z0) | (dy W) act(z0)
+//
+// They work on the fp32 accumulator, so that each result is rounded once and
+// no pre-activation makes a round trip through HBM (u is stored as z only
+// where the backward pass will need it).  A gated forward tile holds 128
+// columns of u0 and the 128 columns of u1 that they meet: the two CTAs of a
+// pair each load one of them as their half of B, and as every CTA's
+// accumulator has all 256 columns, a thread finds both factors in its own
+// TMEM lane.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -33,6 +47,7 @@
 #include <mutex>
 #include <unordered_map>
 
+#include "gl_act.cuh"
 #include "gl_internal.h"
 #include "gl_ptx.cuh"
 
@@ -48,6 +63,9 @@ constexpr int kSmemBudget = 212992;  // stage ring (pairs: 3 x 64 KB; single CTA
 // 14336-wide layer), so it keeps 8, as does wgrad (no measured difference).
 template <int MODE>
 __host__ __device__ constexpr int band_rows() { return MODE == kFwd ? 16 : 8; }
+
+// Epilogue forms of FWD and DGRAD.
+enum { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2 };
 
 template <int MODE, int CG>
 struct Cfg {
@@ -99,7 +117,19 @@ struct GemmParams {
   int accumulate;
   uint64_t wait_ns;  // bound on each pipeline wait
   int hold_loads;    // testing: the producer issues no loads
+  int act;                        // inner activation of the epilogue forms
+  const __nv_bfloat16* residual;  // FWD forms: [M, columns of y] or null
+  __nv_bfloat16* z;               // FWD forms: pre-activations [M, N], written, or null; DGRAD forms: read
 };
+
+// Columns of a tile's output (and its extent): a gated forward tile of 256
+// accumulator columns yields 128.
+template <int MODE, int EPI>
+__device__ __forceinline__ int out_cols(const GemmParams& p) {
+  return MODE == kFwd ? (EPI == kEpiGated ? p.N / 2 : p.N) : p.K;
+}
+template <int MODE, int EPI>
+__host__ __device__ constexpr int out_tile() { return (MODE == kFwd && EPI == kEpiGated) ? 128 : 256; }
 
 template <bool PG>
 struct PGArgs {
@@ -127,15 +157,15 @@ struct Tile {
 
 __device__ __forceinline__ int ceil_div_i(int64_t a, int b) { return static_cast<int>((a + b - 1) / b); }
 
-template <int MODE, int CG>
+template <int MODE, int CG, int EPI>
 __device__ __forceinline__ int tiles_of_group(int64_t m, const GemmParams& p) {
   using C = Cfg<MODE, CG>;
-  if (MODE == kFwd) return m > 0 ? ceil_div_i(m, C::kTileM) * ceil_div_i(p.N, C::kTileN) : 0;
-  if (MODE == kDgrad) return m > 0 ? ceil_div_i(m, C::kTileM) * ceil_div_i(p.K, C::kTileN) : 0;
+  if (MODE != kWgrad)
+    return m > 0 ? ceil_div_i(m, C::kTileM) * ceil_div_i(out_cols<MODE, EPI>(p), out_tile<MODE, EPI>()) : 0;
   return (m > 0 || !p.accumulate) ? ceil_div_i(p.N, C::kTileM) * ceil_div_i(p.K, C::kTileN) : 0;
 }
 
-template <int MODE, int CG>
+template <int MODE, int CG, int EPI>
 __device__ __forceinline__ Tile decode_tile(int t, const int* prefix, const GemmParams& p) {
   using C = Cfg<MODE, CG>;
   // largest g with prefix[g] <= t (prefix is non-decreasing, prefix[0] = 0)
@@ -153,7 +183,7 @@ __device__ __forceinline__ Tile decode_tile(int t, const int* prefix, const Gemm
   // rows, column-major inside a band, so the ~#SMs tiles in flight cover a
   // near-square block and share operand strips through L2.
   const int mtg = (MODE == kWgrad) ? ceil_div_i(p.N, C::kTileM) : ceil_div_i(m, C::kTileM);
-  const int ntg = ceil_div_i(MODE == kFwd ? p.N : p.K, C::kTileN);
+  const int ntg = ceil_div_i(out_cols<MODE, EPI>(p), out_tile<MODE, EPI>());
   constexpr int kBand = band_rows<MODE>();
   const int band = local / (kBand * ntg);
   const int base_mt = band * kBand;
@@ -213,7 +243,113 @@ __device__ __forceinline__ void zero_tail_rows(uint8_t* sa, uint8_t* sb, int r_f
   fence_proxy_async_smem();
 }
 
-template <int MODE, int CG, bool PG>
+// Eight consecutive bf16 values as fp32 (plain loads: y may be the residual's
+// buffer).
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(&w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __bfloat162float(b[j]);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  uint4 w;
+  w.x = pack_bf16x2(v[0], v[1]);
+  w.y = pack_bf16x2(v[2], v[3]);
+  w.z = pack_bf16x2(v[4], v[5]);
+  w.w = pack_bf16x2(v[6], v[7]);
+  *reinterpret_cast<uint4*>(p) = w;
+}
+
+// 32 accumulator columns of this thread's TMEM lane.
+__device__ __forceinline__ void load_acc32(uint32_t taddr, uint32_t (&r)[32]) {
+  tmem_ld_32x32b_x32(taddr, r);
+  tmem_ld_wait();
+  tmem_reg_fence(r);
+}
+
+// One thread's part of a tile in the forms kEpiAct / kEpiGated: its row's
+// columns [n0, n0 + out_tile), 32 at a time.  `release` is called once the
+// accumulator has been read.
+template <int MODE, int EPI, typename Release>
+__device__ __forceinline__ void epilogue_act(const GemmParams& p, uint32_t tacc, int64_t row, bool row_ok, int n0,
+                                             const __nv_bfloat16* bias, Release release) {
+  constexpr int kOut = out_tile<MODE, EPI>();
+  const int F = out_cols<MODE, EPI>(p);  // columns of y (FWD) or of dy W (DGRAD)
+  const int width = (EPI == kEpiGated && MODE == kDgrad) ? 2 * F : F;
+  const int64_t zw = (MODE == kFwd) ? p.N : width;  // columns of z
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + row * width;
+  __nv_bfloat16* z = p.z + row * zw;
+  const __nv_bfloat16* res = p.residual + row * F;
+  const int nchunks = min(kOut / 32, ceil_div_i(F - n0, 32));
+  for (int c = 0; c < nchunks; ++c) {
+    const int n = n0 + c * 32;
+    uint32_t r[32], r1[EPI == kEpiGated && MODE == kFwd ? 32 : 1];
+    load_acc32(tacc + c * 32, r);
+    if constexpr (EPI == kEpiGated && MODE == kFwd) load_acc32(tacc + kOut + c * 32, r1);
+    if (c == nchunks - 1) release();
+#pragma unroll
+    for (int j8 = 0; j8 < 4; ++j8) {
+      const int nn = n + j8 * 8;
+      if (nn >= F || !row_ok) continue;  // F % 8 == 0: eight columns are all in or all out
+      float u[8], a[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = __uint_as_float(r[j8 * 8 + j]);
+      if constexpr (MODE == kFwd) {
+        if (bias != nullptr) {
+          load8(bias + nn, a);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] += a[j];
+        }
+        if (p.z != nullptr) store8(z + nn, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = act_value(p.act, u[j]);
+        if constexpr (EPI == kEpiGated) {
+          float u1[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u1[j] = __uint_as_float(r1[j8 * 8 + j]);
+          if (bias != nullptr) {
+            load8(bias + F + nn, a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u1[j] += a[j];
+          }
+          if (p.z != nullptr) store8(z + F + nn, u1);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] *= u1[j];
+        }
+        if (p.residual != nullptr) {
+          load8(res + nn, a);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] += a[j];
+        }
+        store8(out + nn, u);
+      } else {
+        load8(z + nn, a);
+        if constexpr (EPI == kEpiGated) {
+          float z1[8], d1[8];
+          load8(z + F + nn, z1);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float value;
+            const float slope = act_slope(p.act, a[j], value);
+            d1[j] = u[j] * value;
+            u[j] *= z1[j] * slope;
+          }
+          store8(out + F + nn, d1);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float value;
+            u[j] *= act_slope(p.act, a[j], value);
+          }
+        }
+        store8(out + nn, u);
+      }
+    }
+  }
+}
+
+template <int MODE, int CG, bool PG, int EPI>
 __global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ PGArgs<PG> pg) {
   using C = Cfg<MODE, CG>;
@@ -275,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
       int cnt = 0;
       if (i < p.G) {
         const int64_t m = __ldg(p.offsets + i + 1) - __ldg(p.offsets + i);
-        cnt = tiles_of_group<MODE, CG>(m, p);
+        cnt = tiles_of_group<MODE, CG, EPI>(m, p);
       }
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -314,7 +450,7 @@ __global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
       uint32_t phase = 0;
       int issued = 0;
       for (int t = pair; t < total && !*abort_flag; t += npairs) {
-        const Tile tl = decode_tile<MODE, CG>(t, prefix, p);
+        const Tile tl = decode_tile<MODE, CG, EPI>(t, prefix, p);
         for (int kb = 0; kb < tl.num_kb; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.wait_ns)) { report_abort(abort_flag, p.status); break; }
           if (p.hold_loads) {  // testing the timeout path: this stage never lands
@@ -329,7 +465,17 @@ __global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < C::kBK / 64; ++c) {
               tma_load_2d(sa + c * 16384, &p.tmA, &full[stage], kb * C::kBK + c * 64, static_cast<int32_t>(tl.r0 + hr));
-              if (PG) tma_load_2d(sb + c * C::kBRows * 128, pg.map(tl.g), &full[stage], kb * C::kBK + c * 64, n0);
+              if constexpr (EPI == kEpiGated) {
+                // accumulator columns 0-127: rows nt * 128 .. of W's first half; 128-255: of its second.
+                // (Rows past the first half's end belong to the second: their columns are not stored.)
+                for (int h = 0; h < 2 / CG; ++h) {
+                  const int half = (CG == 2) ? static_cast<int>(rank) : h;
+                  const int nr = half * (p.N / 2) + tl.nt * 128;
+                  uint8_t* dst = sb + c * C::kBRows * 128 + h * 16384;
+                  if (PG) tma_load_2d(dst, pg.map(tl.g), &full[stage], kb * C::kBK + c * 64, nr);
+                  else    tma_load_3d(dst, &p.tmB, &full[stage], kb * C::kBK + c * 64, nr, tl.g);
+                }
+              } else if (PG) tma_load_2d(sb + c * C::kBRows * 128, pg.map(tl.g), &full[stage], kb * C::kBK + c * 64, n0);
               else    tma_load_3d(sb + c * C::kBRows * 128, &p.tmB, &full[stage], kb * C::kBK + c * 64, n0, tl.g);
             }
           } else if (MODE == kDgrad) {
@@ -378,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
       uint32_t phase = 0;
       int it = 0;
       for (int t = pair; t < total; t += npairs, ++it) {
-        const Tile tl = decode_tile<MODE, CG>(t, prefix, p);
+        const Tile tl = decode_tile<MODE, CG, EPI>(t, prefix, p);
         const int buf = it & 1;
         const uint32_t tph = (it >> 1) & 1;
         // every lane waits; the warp acts on a unanimous result
@@ -468,7 +614,7 @@ __global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       for (int t = pair; t < total; t += npairs) {
-        const Tile tl = decode_tile<MODE, CG>(t, prefix, p);
+        const Tile tl = decode_tile<MODE, CG, EPI>(t, prefix, p);
         bool ok = true;
         for (int kb = 0; kb < tl.num_kb; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, p.wait_ns))) {
@@ -513,7 +659,7 @@ __global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
     };
     int it = 0;
     for (int t = pair; t < total; t += npairs, ++it) {
-      const Tile tl = decode_tile<MODE, CG>(t, prefix, p);
+      const Tile tl = decode_tile<MODE, CG, EPI>(t, prefix, p);
       const int buf = it & 1;
       const uint32_t tph = (it >> 1) & 1;
       if (MODE == kWgrad && p.accumulate) {
@@ -537,7 +683,13 @@ __global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
         }
       };
 
-      if (MODE != kWgrad) {
+      if constexpr (MODE != kWgrad && EPI != kEpiPlain) {
+        const int64_t row = tl.r0 + hr + row_in_tile;
+        const bool row_ok = row >= 0 && row < tl.r1 && row < p.M && row < p.out_rows;
+        const __nv_bfloat16* bias = nullptr;
+        if (MODE == kFwd && p.has_bias) bias = PG ? pg.b(tl.g) : (p.bias + static_cast<int64_t>(tl.g) * p.N);
+        epilogue_act<MODE, EPI>(p, tacc, row, row_ok, tl.nt * out_tile<MODE, EPI>(), bias, release_acc);
+      } else if (MODE != kWgrad) {
         const int Nout = (MODE == kFwd) ? p.N : p.K;
         const int64_t row = tl.r0 + hr + row_in_tile;
         const bool row_ok = row >= 0 && row < tl.r1 && row < p.out_rows;
@@ -703,10 +855,10 @@ int grid_for(Kern kern, int cg, int threads, int smem) {
   return grid;
 }
 
-template <int MODE, int CG, bool PG>
+template <int MODE, int CG, int EPI, bool PG>
 gl_status launch_one(const GemmParams& prm, const PGArgs<PG>& pga, int G, cudaStream_t stream) {
   const int smem = smem_bytes_for<MODE, CG>(G);
-  auto kern = grouped_gemm_kernel<MODE, CG, PG>;
+  auto kern = grouped_gemm_kernel<MODE, CG, PG, EPI>;
   if (set_max_smem(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return GL_ERR_CUDA;
   constexpr int threads = Cfg<MODE, CG>::kThreads;
   const int grid = grid_for(kern, CG, threads, smem);
@@ -720,7 +872,7 @@ gl_status launch_one(const GemmParams& prm, const PGArgs<PG>& pga, int G, cudaSt
   return cudaGetLastError() == cudaSuccess ? GL_OK : GL_ERR_CUDA;
 }
 
-template <int MODE, int CG>
+template <int MODE, int CG, int EPI = kEpiPlain>
 gl_status launch_mode(const GemmCall& c) {
   using Cf = Cfg<MODE, CG>;
   const CUtensorMapDataType BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -736,6 +888,11 @@ gl_status launch_mode(const GemmCall& c) {
   prm.wait_ns = c.wait_ns ? c.wait_ns : kWaitLimitNs;
   prm.hold_loads = c.hold_loads;
   prm.has_bias = (MODE == kFwd && c.bias != nullptr) ? 1 : 0;
+  prm.act = act_inner(c.act);
+  prm.residual = static_cast<const __nv_bfloat16*>(c.residual);
+  prm.z = static_cast<__nv_bfloat16*>(c.z);
+  // a gated forward loads W in boxes of 128 rows, whatever the tile shape
+  constexpr uint32_t kWBox = (MODE == kFwd && EPI == kEpiGated) ? 128 : Cf::kBRows;
   const uint64_t Mrows = c.M > 0 ? static_cast<uint64_t>(c.M) : 1;  // a map needs >= 1 row
   bool ok = true;
   if (MODE == kFwd) {
@@ -751,7 +908,7 @@ gl_status launch_mode(const GemmCall& c) {
   const bool stacked = (MODE == kWgrad) ? (c.out_grouped.mode == GL_STACKED) : (c.w.mode == GL_STACKED);
   const bool bias_stacked = prm.has_bias && c.bias->mode == GL_STACKED;
   if (stacked && (!prm.has_bias || bias_stacked)) {
-    if (MODE == kFwd) ok &= make_3d(&prm.tmB, c.w.base, c.K, c.N, c.G, BK, Cf::kBRows, BF, 2);
+    if (MODE == kFwd) ok &= make_3d(&prm.tmB, c.w.base, c.K, c.N, c.G, BK, kWBox, BF, 2);
     if (MODE == kDgrad) ok &= make_3d(&prm.tmB, c.w.base, c.K, c.N, c.G, 64, Cf::kBK, BF, 2);
     if (MODE == kWgrad) prm.mg = static_cast<float*>(const_cast<void*>(c.out_grouped.base));
     if (!ok) return GL_ERR_UNSUPPORTED;
@@ -759,7 +916,7 @@ gl_status launch_mode(const GemmCall& c) {
     prm.G = c.G;
     if (prm.has_bias) prm.bias = reinterpret_cast<const __nv_bfloat16*>(c.bias->base);
     PGArgs<false> none{0};
-    return launch_one<MODE, CG, false>(prm, none, c.G, c.stream);
+    return launch_one<MODE, CG, EPI>(prm, none, c.G, c.stream);
   }
   // Per-group pointers (weights, biases or main_grad): launches of <= kPG groups.
   PGArgs<true>* pga = new PGArgs<true>;
@@ -773,7 +930,7 @@ gl_status launch_mode(const GemmCall& c) {
         const void* wp = (c.w.mode == GL_STACKED)
                              ? static_cast<const uint8_t*>(c.w.base) + static_cast<size_t>(g) * c.N * c.K * 2
                              : c.w.ptrs[g];
-        if (MODE == kFwd) ok &= make_2d(&pga->tm[i], wp, c.K, c.N, BK, Cf::kBRows, BF, 2);
+        if (MODE == kFwd) ok &= make_2d(&pga->tm[i], wp, c.K, c.N, BK, kWBox, BF, 2);
         else              ok &= make_2d(&pga->tm[i], wp, c.K, c.N, 64, Cf::kBK, BF, 2);
         if (prm.has_bias)
           pga->bias[i] = reinterpret_cast<const __nv_bfloat16*>(
@@ -790,20 +947,26 @@ gl_status launch_mode(const GemmCall& c) {
     if (!ok) { st = GL_ERR_UNSUPPORTED; break; }
     prm.offsets = c.offsets + g0;
     prm.G = cg;
-    st = launch_one<MODE, CG, true>(prm, *pga, cg, c.stream);
+    st = launch_one<MODE, CG, EPI>(prm, *pga, cg, c.stream);
   }
   delete pga;
   return st;
 }
 
-template <int MODE>
+template <int MODE, int EPI = kEpiPlain>
 gl_status launch_cg(const GemmCall& c) {
-  return c.cta_pair ? launch_mode<MODE, 2>(c) : launch_mode<MODE, 1>(c);
+  return c.cta_pair ? launch_mode<MODE, 2, EPI>(c) : launch_mode<MODE, 1, EPI>(c);
 }
 
 }  // namespace
 
 gl_status launch_grouped_gemm(const GemmCall& c) {
+  if (c.epilogue) {
+    const bool gated = act_gated(c.act);
+    if (c.mode == kFwd) return gated ? launch_cg<kFwd, kEpiGated>(c) : launch_cg<kFwd, kEpiAct>(c);
+    if (c.mode == kDgrad) return gated ? launch_cg<kDgrad, kEpiGated>(c) : launch_cg<kDgrad, kEpiAct>(c);
+    return GL_ERR_INVALID;
+  }
   switch (c.mode) {
     case kFwd: return launch_cg<kFwd>(c);
     case kDgrad: return launch_cg<kDgrad>(c);

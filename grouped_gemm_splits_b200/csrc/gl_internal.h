@@ -43,6 +43,10 @@ struct GemmCall {
   uint64_t wait_ns;  // bound on each pipeline wait inside the kernel
   int hold_loads;    // testing: issue no loads (every pipeline wait runs out)
   cudaStream_t stream;
+  int epilogue;          // 1: gl_fwd_act / gl_dgrad_act (the fields below)
+  int act;               // GL_ACT_*
+  const void* residual;  // FWD: added after the activation (nullable)
+  void* z;               // FWD: pre-activations out (nullable); DGRAD: pre-activations in
 };
 
 gl_status launch_grouped_gemm(const GemmCall& c);

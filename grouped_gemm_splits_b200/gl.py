@@ -22,11 +22,14 @@ GL_OK, GL_ERR_INVALID, GL_ERR_UNSUPPORTED, GL_ERR_CUDA = 0, 1, 2, 3
 GL_DEV_NEG_SPLIT, GL_DEV_SUM_MISMATCH, GL_DEV_OUT_OVERFLOW, GL_DEV_TIMEOUT = 1, 2, 4, 8
 GL_STACKED, GL_PER_GROUP = 0, 1
 GL_SCALES_ROWMAJOR, GL_SCALES_MMA = 0, 1
+(GL_ACT_NONE, GL_ACT_RELU, GL_ACT_RELU2, GL_ACT_GELU, GL_ACT_SILU, GL_ACT_SWIGLU, GL_ACT_GEGLU) = range(7)
+ACTS = {"none": GL_ACT_NONE, "relu": GL_ACT_RELU, "relu2": GL_ACT_RELU2, "gelu": GL_ACT_GELU, "silu": GL_ACT_SILU,
+        "swiglu": GL_ACT_SWIGLU, "geglu": GL_ACT_GEGLU}
 
 EXPORTED = ("gl_version", "gl_status_string", "gl_offsets", "gl_fwd", "gl_dgrad", "gl_wgrad",
             "gl_dbias", "group_quantize_mxfp8", "gl_mxfp8_scale_bytes", "gl_dbias_workspace_bytes",
             "group_quantize_mxfp8_dbias", "gl_fwd_mxfp8", "gl_dgrad_mxfp8", "gl_wgrad_mxfp8",
-            "gl_rmsnorm", "gl_rmsnorm_bwd", "gl_rmsnorm_bwd_workspace_bytes")
+            "gl_fwd_act", "gl_dgrad_act", "gl_rmsnorm", "gl_rmsnorm_bwd", "gl_rmsnorm_bwd_workspace_bytes")
 
 
 class GlGrouped(ctypes.Structure):
@@ -91,6 +94,11 @@ def load() -> ctypes.CDLL:
     L.gl_dgrad_mxfp8.argtypes = [vp, vp, GlGrouped, GlGrouped, vp, vp, i32, i64, i32, i32, vp, i64, op, vp]
     L.gl_wgrad_mxfp8.restype = i32
     L.gl_wgrad_mxfp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, GlGrouped, i32, op, vp]
+    L.gl_fwd_act.restype = i32
+    L.gl_fwd_act.argtypes = [vp, GlGrouped, ctypes.POINTER(GlGrouped), vp, i32, vp, vp, i32, i64, i32, i32, vp, vp, i64,
+                             op, vp]
+    L.gl_dgrad_act.restype = i32
+    L.gl_dgrad_act.argtypes = [vp, GlGrouped, vp, i32, vp, vp, i32, i64, i32, i32, vp, i64, op, vp]
     L.gl_rmsnorm.restype = i32
     L.gl_rmsnorm.argtypes = [vp, vp, vp, ctypes.c_float, i64, i32, vp, vp, vp, vp, vp, i32, vp]
     L.gl_rmsnorm_bwd.restype = i32
@@ -526,3 +534,109 @@ def gl_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, gamma: torch.Tensor, rst
                                      rows, cols, dx.data_ptr(), dgamma.data_ptr(), 1 if accumulate else 0,
                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream), what)
     return dx, dgamma
+
+
+# ------------------------------------- products with an activation in the epilogue
+
+def _gated(act: int) -> bool:
+    return act in (GL_ACT_SWIGLU, GL_ACT_GEGLU)
+
+
+def _weights(what: str, name: str, w: TensorOrList, G: int, *shapes) -> torch.Tensor:
+    """Check a stacked tensor or a list of G tensors of the given per-group shape; returns one of them."""
+    if isinstance(w, torch.Tensor):
+        _tensor(what, name, w, torch.bfloat16, *[(G, *s) for s in shapes])
+        return w
+    _need(len(w) == G, what, f"{name} must have {G} tensors, not {len(w)}")
+    for t in w:
+        _tensor(what, name, t, torch.bfloat16, *shapes)
+        _need(t.device == w[0].device, what, f"{name} on {w[0].device} and {t.device}")
+    return w[0]
+
+
+def _plan(what: str, offsets: torch.Tensor, status: torch.Tensor) -> int:
+    _need(isinstance(offsets, torch.Tensor) and offsets.dim() == 1 and offsets.numel() >= 2, what,
+          "offsets must be the [G + 1] tensor of gl_offsets")
+    _tensor(what, "offsets", offsets, torch.int64, tuple(offsets.shape))
+    _tensor(what, "status", status, torch.int32, (1,), ())
+    return offsets.numel() - 1
+
+
+def _rows_at_least(what: str, name: str, t: torch.Tensor, rows: int, cols: int) -> None:
+    _need(isinstance(t, torch.Tensor) and t.dim() == 2 and t.shape[0] >= rows, what,
+          f"{name} must have at least {rows} rows")
+    _tensor(what, name, t, torch.bfloat16, (t.shape[0], cols))
+
+
+def gl_fwd_act(x: torch.Tensor, w: TensorOrList, bias: Optional[TensorOrList], offsets: torch.Tensor,
+               status: torch.Tensor, act: int, residual: Optional[torch.Tensor] = None, save_z: bool = False,
+               z: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, pair: bool = True,
+               wait_limit_us: int = 0, opt_flags: int = 0):
+    """:func:`gl_fwd` with an activation (``GL_ACT_*``) and a residual in its
+    epilogue: y = act(x W^T + b) + residual, or, gated, act(u0) * u1 + residual
+    on the halves of u = x W^T + b.  Returns (y, z): z is u (bf16 [M, N]), what
+    :func:`gl_dgrad_act` reads, if ``save_z`` is set or a ``z`` is given, else
+    None.  ``y`` may have more rows than x; only the valid ones are written.
+    """
+    what = "gl_fwd_act"
+    G = _plan(what, offsets, status)
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2, what, "x must be a [rows, K] tensor")
+    M, K = x.shape
+    _tensor(what, "x", x, torch.bfloat16, (M, K))
+    _need(act in ACTS.values(), what, f"unknown activation {act}")
+    N = _shape_nk(w)[0]
+    _need(not _gated(act) or N % 2 == 0, what, f"a gated activation halves {N} columns")
+    w0 = _weights(what, "w", w, G, (N, K))
+    b0 = _weights(what, "bias", bias, G, (N,)) if bias is not None else None
+    Nout = N // 2 if _gated(act) else N
+    if residual is not None:
+        _tensor(what, "residual", residual, torch.bfloat16, (M, Nout))
+    if z is not None:
+        _tensor(what, "z", z, torch.bfloat16, (M, N))
+    if y is not None:
+        _rows_at_least(what, "y", y, M, Nout)
+    with _On(what, x, w0, b0, residual, offsets, status, z, y) as stream:
+        if y is None:
+            y = torch.empty(M, Nout, dtype=torch.bfloat16, device=x.device)
+        if z is None and save_z:
+            z = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        wg, keep_w = _grouped(w, G)
+        bptr, keep_b = None, None
+        if bias is not None:
+            bg, keep_b = _grouped(bias, G)
+            bptr = ctypes.pointer(bg)
+        _check(load().gl_fwd_act(x.data_ptr(), wg, bptr, _ptr(residual), act, offsets.data_ptr(), status.data_ptr(),
+                                 G, M, N, K, _ptr(z), y.data_ptr(), y.shape[0], _opts(pair, wait_limit_us, opt_flags),
+                                 stream), what)
+    del keep_w, keep_b
+    return y, z
+
+
+def gl_dgrad_act(dy: torch.Tensor, w: TensorOrList, z: torch.Tensor, offsets: torch.Tensor, status: torch.Tensor,
+                 act: int, dz: Optional[torch.Tensor] = None, pair: bool = True, wait_limit_us: int = 0,
+                 opt_flags: int = 0) -> torch.Tensor:
+    """:func:`gl_dgrad` that goes on through the activation in front of the
+    product: dz = (dy W) * act'(z), with z from the :func:`gl_fwd_act` before
+    ([M, K], or [M, 2K] for a gated activation, whose dz has both factors'
+    gradients)."""
+    what = "gl_dgrad_act"
+    G = _plan(what, offsets, status)
+    _need(isinstance(dy, torch.Tensor) and dy.dim() == 2, what, "dy must be a [rows, N] tensor")
+    M, N = dy.shape
+    _tensor(what, "dy", dy, torch.bfloat16, (M, N))
+    _need(act in ACTS.values() and act != GL_ACT_NONE, what, f"activation {act} has no slope to apply")
+    K = _shape_nk(w)[1]
+    w0 = _weights(what, "w", w, G, (N, K))
+    width = 2 * K if _gated(act) else K
+    _tensor(what, "z", z, torch.bfloat16, (M, width))
+    if dz is not None:
+        _rows_at_least(what, "dz", dz, M, width)
+    with _On(what, dy, w0, z, offsets, status, dz) as stream:
+        if dz is None:
+            dz = torch.empty(M, width, dtype=torch.bfloat16, device=dy.device)
+        wg, keep = _grouped(w, G)
+        _check(load().gl_dgrad_act(dy.data_ptr(), wg, z.data_ptr(), act, offsets.data_ptr(), status.data_ptr(), G, M,
+                                   N, K, dz.data_ptr(), dz.shape[0], _opts(pair, wait_limit_us, opt_flags), stream),
+               what)
+    del keep
+    return dz

@@ -389,6 +389,58 @@ gl_status gl_wgrad_mxfp8(const uint8_t* x_codes_c, const uint8_t* x_scales_c, co
                          int64_t M, int N, int K, gl_grouped main_grad, int accumulate, const gl_gemm_opts* opts, void* stream);
 
 /*
+ * gl_fwd_act -- gl_fwd with an activation and a residual in its epilogue:
+ *     u = x_i W_i^T (+ b_i)
+ *     y = act(u) (+ residual)                         GL_ACT_NONE .. GL_ACT_SILU
+ *     y = act(u[:, :F]) * u[:, F:] (+ residual)       GL_ACT_SWIGLU, GL_ACT_GEGLU; F = N / 2
+ * The first product of an expert with its activation, or the second with the
+ * residual stream.  Everything past the product is computed on the fp32
+ * accumulator; each output is rounded once.
+ *
+ *   x, w, bias, offsets, status, opts   as for gl_fwd; w [N, K] of a gated
+ *             activation holds the F rows of the activated factor first
+ *   residual  NULL or device bf16 [M, columns of y]
+ *   act       GL_ACT_*
+ *   z         NULL or device bf16 [M, N], written: u, which gl_dgrad_act of
+ *             the next product reads
+ *   y         device bf16 [y_rows, N] ([y_rows, F] when gated), y_rows >= M;
+ *             rows [M, y_rows) are not written; may be the same buffer as
+ *             residual
+ * Limits: those of gl_fwd, and N % 16 == 0 when gated.
+ */
+#define GL_ACT_NONE 0
+#define GL_ACT_RELU 1
+#define GL_ACT_RELU2 2  /* max(u, 0)^2                                         */
+#define GL_ACT_GELU 3   /* 0.5 u (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3)))     */
+#define GL_ACT_SILU 4   /* u / (1 + e^-u)                                      */
+#define GL_ACT_SWIGLU 5 /* silu(u0) * u1                                       */
+#define GL_ACT_GEGLU 6  /* gelu(u0) * u1                                       */
+gl_status gl_fwd_act(const void* x, gl_grouped w, const gl_grouped* bias, const void* residual, int act,
+                     const int64_t* offsets, int32_t* status, int G, int64_t M, int N, int K, void* z,
+                     void* y, int64_t y_rows, const gl_gemm_opts* opts, void* stream);
+
+/*
+ * gl_dgrad_act -- gl_dgrad that goes on through the activation in front of
+ * the product: with dh = dy_i W_i, the gradient of the product's input
+ * h = act(z),
+ *     dz = dh * act'(z)                                            (z, dz [M, K])
+ *     dz = dh * z1 * act'(z0) | dh * act(z0), z = z0 | z1 gated    (z, dz [M, 2K])
+ * z is what gl_fwd_act of the product before wrote; dz is that product's dy
+ * (for gl_dgrad, gl_wgrad and gl_dbias).  The gradient of a residual added by
+ * gl_fwd_act is its dy, unchanged.
+ *
+ *   dy, w, offsets, status, opts   as for gl_dgrad
+ *   act      GL_ACT_RELU .. GL_ACT_GEGLU (GL_ACT_NONE is gl_dgrad)
+ *   z        device bf16 [M, K] ([M, 2K] when gated)
+ *   dz       device bf16 [dz_rows, K] ([dz_rows, 2K]), dz_rows >= M; rows
+ *            [M, dz_rows) are not written; not the same buffer as z
+ * relu's slope at 0 is 0.  Limits: those of gl_dgrad.
+ */
+gl_status gl_dgrad_act(const void* dy, gl_grouped w, const void* z, int act, const int64_t* offsets,
+                       int32_t* status, int G, int64_t M, int N, int K, void* dz, int64_t dz_rows,
+                       const gl_gemm_opts* opts, void* stream);
+
+/*
  * gl_rmsnorm -- root-mean-square norm of the rows of a residual stream, with
  * the residual's addition before it and bf16 and / or MXFP8 output: the norm
  * in front of a grouped linear layer, its MXFP8 form being the x operand of

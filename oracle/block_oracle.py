@@ -35,3 +35,64 @@ def rmsnorm_bwd(dy: np.ndarray, s: np.ndarray, gamma: np.ndarray, rstd: np.ndarr
     if dsum is not None:
         dx = dx + dsum
     return dx, np.sum(dy * xh, axis=0)
+
+
+# ---------------------------------------------------------------- activations
+
+ACTS = ("none", "relu", "relu2", "gelu", "silu", "swiglu", "geglu")
+GATED = {"swiglu": "silu", "geglu": "gelu"}
+
+
+def act(name: str, u: np.ndarray) -> np.ndarray:
+    """An activation of the last dimension (gated ones halve it)."""
+    u = np.asarray(u, dtype=np.float64)
+    if name == "none":
+        return u
+    if name == "relu":
+        return np.maximum(u, 0)
+    if name == "relu2":
+        return np.maximum(u, 0) ** 2
+    if name == "gelu":
+        return 0.5 * u * (1 + np.tanh(math.sqrt(2 / math.pi) * (u + 0.044715 * u ** 3)))
+    if name == "silu":
+        return u * 0.5 * (1 + np.tanh(0.5 * u))
+    F = u.shape[-1] // 2
+    return act(GATED[name], u[..., :F]) * u[..., F:]
+
+
+def slope(name: str, u: np.ndarray) -> np.ndarray:
+    """Derivative of an activation of one argument (0 for relu at 0)."""
+    u = np.asarray(u, dtype=np.float64)
+    if name == "none":
+        return np.ones_like(u)
+    if name == "relu":
+        return (u > 0).astype(np.float64)
+    if name == "relu2":
+        return 2 * np.maximum(u, 0)
+    if name == "silu":
+        q = 0.5 * (1 + np.tanh(0.5 * u))
+        return q + u * q * (1 - q)
+    c = math.sqrt(2 / math.pi)
+    t = np.tanh(c * (u + 0.044715 * u ** 3))
+    return 0.5 * (1 + t) + 0.5 * u * (1 - t * t) * c * (1 + 3 * 0.044715 * u * u)
+
+
+def act_bwd(name: str, z: np.ndarray, dh: np.ndarray) -> np.ndarray:
+    """Gradient of an activation's input for the gradient of its output."""
+    if name not in GATED:
+        return dh * slope(name, z)
+    F = z.shape[-1] // 2
+    g, u = z[..., :F], z[..., F:]
+    return np.concatenate([dh * u * slope(GATED[name], g), dh * act(GATED[name], g)], axis=-1)
+
+
+def fwd_act(x, w, bias, m_splits, name: str, residual: Optional[np.ndarray]):
+    """(y, u): the grouped product u, and act(u) + residual."""
+    u = orc.fwd(x, w, bias, m_splits)
+    y = act(name, u)
+    return (y if residual is None else y + residual), u
+
+
+def dgrad_act(dy, w, m_splits, name: str, z: np.ndarray) -> np.ndarray:
+    """Gradient of the pre-activations z behind the grouped product's input."""
+    return act_bwd(name, z, orc.dgrad(dy, w, m_splits))

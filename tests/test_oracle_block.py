@@ -48,3 +48,42 @@ def test_rmsnorm_by_hand():
     s, rstd, y = blk.rmsnorm(np.array([[3.0, 4.0]]), np.array([[0.0, 0.0]]), np.array([1.0, 2.0]), 0.0)
     assert rstd[0] == pytest.approx(1 / np.sqrt(12.5))
     np.testing.assert_allclose(y, [[3 / np.sqrt(12.5), 8 / np.sqrt(12.5)]])
+
+
+def _torch_act(name, u):
+    F = torch.nn.functional
+    half = u.shape[-1] // 2
+    return {"none": lambda: u, "relu": lambda: F.relu(u), "relu2": lambda: F.relu(u) ** 2,
+            "gelu": lambda: F.gelu(u, approximate="tanh"), "silu": lambda: F.silu(u),
+            "swiglu": lambda: F.silu(u[..., :half]) * u[..., half:],
+            "geglu": lambda: F.gelu(u[..., :half], approximate="tanh") * u[..., half:]}[name]()
+
+
+@pytest.mark.parametrize("name", blk.ACTS)
+def test_activation_and_its_gradient_against_autograd(name):
+    rng = np.random.default_rng(3)
+    u = torch.tensor(rng.standard_normal((9, 24)) * 4, requires_grad=True)
+    y = _torch_act(name, u)
+    dy = torch.tensor(rng.standard_normal(y.shape))
+    (y * dy).sum().backward()
+    np.testing.assert_allclose(blk.act(name, u.detach().numpy()), y.detach().numpy(), rtol=1e-10, atol=1e-13)
+    np.testing.assert_allclose(blk.act_bwd(name, u.detach().numpy(), dy.numpy()), u.grad.numpy(), rtol=1e-9, atol=1e-12)
+
+
+@pytest.mark.parametrize("name", blk.ACTS[1:])
+def test_grouped_products_with_activations_against_autograd(name):
+    rng = np.random.default_rng(4)
+    m = [5, 0, 3]
+    two = 2 if name in blk.GATED else 1
+    x = torch.tensor(rng.standard_normal((8, 6)))
+    z = torch.tensor(rng.standard_normal((8, 10 * two)), requires_grad=True)
+    w = torch.tensor(rng.standard_normal((3, 4, 10)))
+    dy, r = rng.standard_normal((8, 4)), rng.standard_normal((8, 4))
+    h = _torch_act(name, z)
+    y = torch.cat([h[a:b] @ w[g].T for g, (a, b) in enumerate(((0, 5), (5, 5), (5, 8)))]) + torch.tensor(r)
+    (y * torch.tensor(dy)).sum().backward()
+    np.testing.assert_allclose(blk.dgrad_act(dy, w.numpy(), m, name, z.detach().numpy()), z.grad.numpy(), rtol=1e-9,
+                               atol=1e-12)
+    got, u = blk.fwd_act(h.detach().numpy(), w.numpy(), None, m, "none", r)
+    np.testing.assert_allclose(got, y.detach().numpy(), rtol=1e-10)
+    np.testing.assert_allclose(u + r, got, rtol=1e-12)
