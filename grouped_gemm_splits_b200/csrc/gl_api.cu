@@ -569,3 +569,65 @@ gl_status gl_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma, con
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- MoE layer for a few tokens
+namespace {
+
+gl_status check_moe_dims(int T, int E, int k, int H, int F) {
+  if (T < 0 || E <= 0 || k <= 0 || k > E || H <= 0 || F <= 0) return GL_ERR_INVALID;
+  if (T > GL_MOE_MAX_TOKENS || E > GL_MOE_MAX_EXPERTS || k > GL_MOE_MAX_TOP_K) return GL_ERR_UNSUPPORTED;
+  if (H % 8 != 0 || F % 8 != 0 || H > (1 << 20) || F > (1 << 20)) return GL_ERR_UNSUPPORTED;
+  return GL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gl_moe_workspace_bytes(int T, int E, int top_k, int H, int F) {
+  if (check_moe_dims(T, E, top_k, H, F) != GL_OK) return 0;
+  return static_cast<size_t>(gl::moe_workspace_bytes(T, top_k, H, F));
+}
+
+gl_status gl_moe_tokens(const void* x, const void* router, gl_grouped w1, gl_grouped w2, int act, int flags, int T,
+                        int E, int top_k, int H, int F, int32_t* topk_idx, float* topk_w, void* y, int32_t* status,
+                        void* workspace, size_t workspace_bytes, const gl_gemm_opts* opts, void* stream) {
+  const gl_status st = check_moe_dims(T, E, top_k, H, F);
+  if (st != GL_OK) return st;
+  int pair = 1, hold = 0;
+  uint64_t wait_ns = 0;
+  if (!read_opts(opts, &pair, &wait_ns, &hold) || !pair) return GL_ERR_INVALID;
+  if (!gl::act_gated(act) || (flags & ~GL_MOE_RENORM)) return GL_ERR_INVALID;
+  if (!grouped_ok(w1, E) || !grouped_ok(w2, E) || status == nullptr || workspace == nullptr) return GL_ERR_INVALID;
+  if (T > 0 && (x == nullptr || topk_idx == nullptr || topk_w == nullptr || y == nullptr)) return GL_ERR_INVALID;
+  if (workspace_bytes < gl_moe_workspace_bytes(T, E, top_k, H, F)) return GL_ERR_INVALID;
+  if ((w1.mode != GL_STACKED || w2.mode != GL_STACKED) && E > 64) return GL_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(router) || !aligned16(y) || !grouped_aligned(w1, E) || !grouped_aligned(w2, E) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) || (reinterpret_cast<uintptr_t>(topk_idx) & 3u) ||
+      (reinterpret_cast<uintptr_t>(topk_w) & 3u))
+    return GL_ERR_UNSUPPORTED;
+  if (T == 0) return GL_OK;
+  gl::MoeCall c{};
+  c.x = x;
+  c.router = router;
+  c.w1 = w1;
+  c.w2 = w2;
+  c.act = act;
+  c.renorm = flags & GL_MOE_RENORM;
+  c.T = T;
+  c.E = E;
+  c.k = top_k;
+  c.H = H;
+  c.F = F;
+  c.idx = topk_idx;
+  c.w = topk_w;
+  c.y = y;
+  c.status = status;
+  c.workspace = workspace;
+  c.wait_ns = wait_ns;
+  c.hold_loads = hold;
+  c.stream = to_stream(stream);
+  return gl::launch_moe(c);
+}
+
+}  // extern "C"

@@ -115,4 +115,24 @@ gl_status launch_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma,
                              int64_t rows, int cols, void* dx, float* dgamma, int accumulate, float* part,
                              cudaStream_t stream);
 
+// A mixture-of-experts layer for a few tokens (gl_moe.cu).
+struct MoeCall {
+  const void* x;
+  const void* router;  // nullable: idx and w are inputs
+  gl_grouped w1, w2;
+  int act, renorm;
+  int T, E, k, H, F;
+  int32_t* idx;
+  float* w;
+  void* y;
+  int32_t* status;
+  void* workspace;
+  uint64_t wait_ns;
+  int hold_loads;
+  cudaStream_t stream;
+};
+
+int64_t moe_workspace_bytes(int T, int k, int H, int F);
+gl_status launch_moe(const MoeCall& c);
+
 }  // namespace gl

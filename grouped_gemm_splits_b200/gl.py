@@ -20,16 +20,19 @@ _lib = None
 
 GL_OK, GL_ERR_INVALID, GL_ERR_UNSUPPORTED, GL_ERR_CUDA = 0, 1, 2, 3
 GL_DEV_NEG_SPLIT, GL_DEV_SUM_MISMATCH, GL_DEV_OUT_OVERFLOW, GL_DEV_TIMEOUT = 1, 2, 4, 8
+GL_DEV_BAD_INDEX = 16
 GL_STACKED, GL_PER_GROUP = 0, 1
 GL_SCALES_ROWMAJOR, GL_SCALES_MMA = 0, 1
 (GL_ACT_NONE, GL_ACT_RELU, GL_ACT_RELU2, GL_ACT_GELU, GL_ACT_SILU, GL_ACT_SWIGLU, GL_ACT_GEGLU) = range(7)
 ACTS = {"none": GL_ACT_NONE, "relu": GL_ACT_RELU, "relu2": GL_ACT_RELU2, "gelu": GL_ACT_GELU, "silu": GL_ACT_SILU,
         "swiglu": GL_ACT_SWIGLU, "geglu": GL_ACT_GEGLU}
+GL_MOE_MAX_TOKENS, GL_MOE_MAX_EXPERTS, GL_MOE_MAX_TOP_K, GL_MOE_RENORM = 128, 256, 16, 1
 
 EXPORTED = ("gl_version", "gl_status_string", "gl_offsets", "gl_fwd", "gl_dgrad", "gl_wgrad",
             "gl_dbias", "group_quantize_mxfp8", "gl_mxfp8_scale_bytes", "gl_dbias_workspace_bytes",
             "group_quantize_mxfp8_dbias", "gl_fwd_mxfp8", "gl_dgrad_mxfp8", "gl_wgrad_mxfp8",
-            "gl_fwd_act", "gl_dgrad_act", "gl_rmsnorm", "gl_rmsnorm_bwd", "gl_rmsnorm_bwd_workspace_bytes")
+            "gl_fwd_act", "gl_dgrad_act", "gl_rmsnorm", "gl_rmsnorm_bwd", "gl_rmsnorm_bwd_workspace_bytes",
+            "gl_moe_tokens", "gl_moe_workspace_bytes")
 
 
 class GlGrouped(ctypes.Structure):
@@ -105,6 +108,11 @@ def load() -> ctypes.CDLL:
     L.gl_rmsnorm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, vp, i32, vp, ctypes.c_size_t, vp]
     L.gl_rmsnorm_bwd_workspace_bytes.restype = ctypes.c_size_t
     L.gl_rmsnorm_bwd_workspace_bytes.argtypes = [i64, i32]
+    L.gl_moe_tokens.restype = i32
+    L.gl_moe_tokens.argtypes = [vp, vp, GlGrouped, GlGrouped, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp,
+                                ctypes.c_size_t, op, vp]
+    L.gl_moe_workspace_bytes.restype = ctypes.c_size_t
+    L.gl_moe_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     _lib = L
     return L
 
@@ -640,3 +648,69 @@ def gl_dgrad_act(dy: torch.Tensor, w: TensorOrList, z: torch.Tensor, offsets: to
                what)
     del keep
     return dz
+
+
+# -------------------------------------------- a mixture-of-experts layer for a few tokens
+
+def moe_workspace_bytes(T: int, E: int, top_k: int, H: int, F: int) -> int:
+    """Workspace bytes of :func:`gl_moe_tokens` on the current device."""
+    n = load().gl_moe_workspace_bytes(T, E, top_k, H, F)
+    if n == 0:
+        raise GlError(f"gl_moe_workspace_bytes: outside the layer's limits ({T}, {E}, {top_k}, {H}, {F})")
+    return n
+
+
+def gl_moe_tokens(x: torch.Tensor, w1: TensorOrList, w2: TensorOrList, top_k: int, status: torch.Tensor,
+                  router_w: Optional[torch.Tensor] = None, topk_idx: Optional[torch.Tensor] = None,
+                  topk_w: Optional[torch.Tensor] = None, act: int = GL_ACT_SWIGLU, renorm: bool = True,
+                  y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  wait_limit_us: int = 0, opt_flags: int = 0):
+    """A mixture-of-experts layer for up to 128 tokens: y = sum over each
+    token's experts of w * ((act(x W1a^T) * (x W1b^T)) W2^T), W1 = [W1a; W1b].
+
+    With ``router_w`` ([E, H]) the experts are the ``top_k`` largest of
+    softmax(x router_w^T), their weights divided by their sum if ``renorm``;
+    without it ``topk_idx`` (int32 [T, top_k], -1: none) and ``topk_w`` (fp32)
+    are the routing.  ``workspace`` (uint8, at least
+    :func:`moe_workspace_bytes`) is allocated when absent; calls that overlap
+    need one each.  Returns (y, topk_idx, topk_w).
+    """
+    what = "gl_moe_tokens"
+    bf = torch.bfloat16
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2, what, "x must be a [tokens, H] tensor")
+    T, H = x.shape
+    _tensor(what, "x", x, bf, (T, H))
+    _tensor(what, "status", status, torch.int32, (1,), ())
+    E = len(w1)
+    F = _shape_nk(w2)[1]
+    a = _weights(what, "w1", w1, E, (2 * F, H))
+    b = _weights(what, "w2", w2, E, (H, F))
+    _need(T <= GL_MOE_MAX_TOKENS, what, f"{T} tokens: at most {GL_MOE_MAX_TOKENS}")
+    if router_w is not None:
+        _tensor(what, "router_w", router_w, bf, (E, H))
+    else:
+        _need(topk_idx is not None and topk_w is not None, what, "router_w, or topk_idx and topk_w, are required")
+    if topk_idx is not None:
+        _tensor(what, "topk_idx", topk_idx, torch.int32, (T, top_k))
+    if topk_w is not None:
+        _tensor(what, "topk_w", topk_w, torch.float32, (T, top_k))
+    if y is not None:
+        _tensor(what, "y", y, bf, (T, H))
+    with _On(what, x, a, b, router_w, status, topk_idx, topk_w, y, workspace) as stream:
+        if topk_idx is None:
+            topk_idx = torch.empty(T, top_k, dtype=torch.int32, device=x.device)
+        if topk_w is None:
+            topk_w = torch.empty(T, top_k, dtype=torch.float32, device=x.device)
+        if y is None:
+            y = torch.empty(T, H, dtype=bf, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(moe_workspace_bytes(T, E, top_k, H, F), dtype=torch.uint8, device=x.device)
+        g1, keep1 = _grouped(w1, E)
+        g2, keep2 = _grouped(w2, E)
+        _check(load().gl_moe_tokens(x.data_ptr(), _ptr(router_w), g1, g2, act, GL_MOE_RENORM if renorm else 0, T, E,
+                                    top_k, H, F, topk_idx.data_ptr(), topk_w.data_ptr(), y.data_ptr(),
+                                    status.data_ptr(), workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), _opts(True, wait_limit_us, opt_flags),
+                                    stream), what)
+    del keep1, keep2
+    return y, topk_idx, topk_w

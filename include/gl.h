@@ -63,6 +63,8 @@ typedef int gl_status;
 #define GL_DEV_SUM_MISMATCH 2 /* sum(m_splits) != expect_rows                  */
 #define GL_DEV_OUT_OVERFLOW 4 /* sum(m_splits) > out_rows                      */
 #define GL_DEV_TIMEOUT 8      /* a kernel abandoned a bounded wait             */
+#define GL_DEV_BAD_INDEX 16   /* gl_moe_tokens was given an expert that is not */
+                              /* there, or one expert twice for one token      */
 
 /* ---- grouped parameter descriptor --------------------------------------- */
 #define GL_STACKED 0   /* base -> [G, rows, cols], group stride rows*cols      */
@@ -507,6 +509,60 @@ gl_status gl_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma, con
 
 /* Workspace bytes for gl_rmsnorm_bwd; 0 for invalid arguments. */
 size_t gl_rmsnorm_bwd_workspace_bytes(int64_t rows, int cols);
+
+/*
+ * gl_moe_tokens -- a whole mixture-of-experts layer for a few tokens (1 ..
+ * GL_MOE_MAX_TOKENS): the form of the layer for decoding, where the grouped
+ * products' 256-row tiles would be nearly empty.  Per token t:
+ *     p = softmax(x_t router^T) over the E experts
+ *     idx[t, :], w[t, :] = the top_k largest p and their experts (of equal
+ *                          ones the lower expert first); with GL_MOE_RENORM
+ *                          w is divided by its sum
+ *     h_i = act(x_t W1_e[0:F]^T) * (x_t W1_e[F:2F]^T),   e = idx[t, i]
+ *     y_t = sum_i w[t, i] * (h_i W2_e^T)
+ * Products accumulate in fp32; h is rounded to bf16 (it is an operand of the
+ * second product), the weighted sum is fp32 and y is rounded once.  Results
+ * are deterministic for a given GPU.
+ *
+ *   x         device bf16 [T, H]
+ *   router    device bf16 [E, H], or NULL: topk_idx and topk_w are then
+ *             inputs (a caller's own routing; any weights).  An index of -1
+ *             is no expert: such a choice adds nothing, and a token without
+ *             any gets zeros (the padding of a captured batch).
+ *   w1        bf16 [E, 2F, H] stacked or E pointers to [2F, H] (the F rows of
+ *             the activated factor first, as for gl_fwd_act)
+ *   w2        bf16 [E, H, F] stacked or E pointers to [H, F]
+ *   act       GL_ACT_SWIGLU or GL_ACT_GEGLU
+ *   flags     0 or GL_MOE_RENORM
+ *   topk_idx  device int32 [T, top_k], written (read when router is NULL)
+ *   topk_w    device fp32 [T, top_k], likewise
+ *   y         device bf16 [T, H], written
+ *   status    device int32 status word (required): non-zero -> nothing
+ *             written.  GL_DEV_BAD_INDEX is ORed in for a given index outside
+ *             -1 .. E - 1 or an expert that a token has twice (y is then not
+ *             written), GL_DEV_TIMEOUT for a wait that ran out (y incomplete).
+ *   workspace device scratch of workspace_bytes >= gl_moe_workspace_bytes(T,
+ *             E, top_k, H, F), 256-byte aligned; its contents on entry do not
+ *             matter.  Calls that can overlap on the GPU need one each.
+ *   opts      NULL or per-call options (tiles must be GL_TILES_PAIR, the default)
+ * A token whose logits hold a NaN gets NaN weights and a NaN y.
+ * Limits: H % 8 == 0, F % 8 == 0, E <= GL_MOE_MAX_EXPERTS (64 when w1 or w2
+ * is per group), top_k <= GL_MOE_MAX_TOP_K and <= E.  T == 0 does nothing.
+ * Two launches, the second a cooperative one: it starts once every SM is free
+ * for one of its blocks.
+ */
+#define GL_MOE_MAX_TOKENS 128
+#define GL_MOE_MAX_EXPERTS 256
+#define GL_MOE_MAX_TOP_K 16
+#define GL_MOE_RENORM 1
+gl_status gl_moe_tokens(const void* x, const void* router, gl_grouped w1, gl_grouped w2, int act, int flags,
+                        int T, int E, int top_k, int H, int F, int32_t* topk_idx, float* topk_w, void* y,
+                        int32_t* status, void* workspace, size_t workspace_bytes, const gl_gemm_opts* opts,
+                        void* stream);
+
+/* Workspace bytes for gl_moe_tokens on the current device; 0 for arguments
+ * outside its limits. */
+size_t gl_moe_workspace_bytes(int T, int E, int top_k, int H, int F);
 
 #ifdef __cplusplus
 }

@@ -96,3 +96,28 @@ def fwd_act(x, w, bias, m_splits, name: str, residual: Optional[np.ndarray]):
 def dgrad_act(dy, w, m_splits, name: str, z: np.ndarray) -> np.ndarray:
     """Gradient of the pre-activations z behind the grouped product's input."""
     return act_bwd(name, z, orc.dgrad(dy, w, m_splits))
+
+
+# ------------------------------------------ a mixture-of-experts layer, few tokens
+
+def route(x: np.ndarray, router: np.ndarray, k: int, renorm: bool):
+    """(idx, w, logits): the k largest of softmax(x router^T), lower index first where equal."""
+    logits = x @ router.T
+    p = np.exp(logits - logits.max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    idx = np.argsort(-p, axis=1, kind="stable")[:, :k]
+    w = np.take_along_axis(p, idx, axis=1)
+    if renorm:
+        w = w / w.sum(axis=1, keepdims=True)
+    return idx, w, logits
+
+
+def experts(x: np.ndarray, idx: np.ndarray, w: np.ndarray, w1, w2, name: str) -> np.ndarray:
+    """sum_i w[t, i] * W2_e act(W1_e x_t), e = idx[t, i] (-1: none)."""
+    y = np.zeros_like(x)
+    for t in range(x.shape[0]):
+        for i in range(idx.shape[1]):
+            e = int(idx[t, i])
+            if e >= 0:
+                y[t] += w[t, i] * (w2[e] @ act(name, w1[e] @ x[t]))
+    return y

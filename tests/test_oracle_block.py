@@ -87,3 +87,38 @@ def test_grouped_products_with_activations_against_autograd(name):
     got, u = blk.fwd_act(h.detach().numpy(), w.numpy(), None, m, "none", r)
     np.testing.assert_allclose(got, y.detach().numpy(), rtol=1e-10)
     np.testing.assert_allclose(u + r, got, rtol=1e-12)
+
+
+def test_routing_by_hand():
+    x = np.array([[1.0, 0.0], [0.0, 2.0], [0.0, 0.0]])
+    router = np.array([[0.0, 1.0], [1.0, 0.0], [0.0, 1.0], [np.log(2.0), 0.0]])
+    idx, w, _ = blk.route(x, router, 2, True)
+    assert idx.tolist() == [[1, 3], [0, 2], [0, 1]]  # ties: the lower expert
+    e = np.e
+    np.testing.assert_allclose(w, [[e / (e + 2), 2 / (e + 2)], [0.5, 0.5], [0.5, 0.5]])
+    _, w, _ = blk.route(x, router, 2, False)
+    np.testing.assert_allclose(w[0], [e / (e + 4), 2 / (e + 4)])
+
+
+def test_experts_against_torch_and_the_grouped_products():
+    rng = np.random.default_rng(9)
+    T, E, k, H, F = 5, 4, 2, 6, 3
+    x, w1, w2 = rng.standard_normal((T, H)), rng.standard_normal((E, 2 * F, H)), rng.standard_normal((E, H, F))
+    idx, w, _ = blk.route(x, rng.standard_normal((E, H)), k, True)
+    y = blk.experts(x, idx, w, w1, w2, "swiglu")
+    want = torch.zeros(T, H, dtype=torch.float64)
+    for t in range(T):
+        for i in range(k):
+            u = torch.tensor(w1[idx[t, i]]) @ torch.tensor(x[t])
+            want[t] += w[t, i] * (torch.tensor(w2[idx[t, i]]) @ (torch.nn.functional.silu(u[:F]) * u[F:]))
+    np.testing.assert_allclose(y, want.numpy(), rtol=1e-10)
+    # the same layer as the grouped products over rows sorted by expert
+    flat = np.argsort(idx.reshape(-1), kind="stable")
+    m = [int((idx == e).sum()) for e in range(E)]
+    h, _ = blk.fwd_act(x[flat // k], w1, None, m, "swiglu", None)
+    o, _ = blk.fwd_act(h, w2, None, m, "none", None)
+    grouped = np.zeros((T, H))
+    np.add.at(grouped, flat // k, o * w.reshape(-1)[flat, None])
+    np.testing.assert_allclose(y, grouped, rtol=1e-10)
+    idx[2] = -1
+    assert not blk.experts(x, idx, w, w1, w2, "swiglu")[2].any()
