@@ -106,63 +106,94 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ float route_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ void st_cluster_u16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 
-// Logits of all tokens over this CTA's part of H into part[T][E]: one warp
-// per 16 experts.  A thread takes 8 consecutive elements of its expert row
-// and of its token row and uses them as the k pairs of two MMAs: the order of
-// a contraction is free, as long as both operands share it.
-__device__ __forceinline__ void route_logits(const RouteParams& p, float* part, int rank, int warp, int lane) {
+// How a CTA's warps share its logits: units of 16 experts x 32 tokens, and,
+// while there are fewer of them than warps, `ks` parts of the CTA's slice of H.
+struct RouteSplit {
+  int et, tg, ks;
+};
+__host__ __device__ __forceinline__ RouteSplit route_split(int T, int E) {
+  RouteSplit r;
+  r.et = (E + 15) / 16;
+  r.tg = (T + 31) / 32;
+  const int units = r.et * r.tg;
+  r.ks = units >= kRouteWarps ? 1 : kRouteWarps / units;
+  return r;
+}
+
+// Logits of all tokens over this CTA's part of H into part[ks][T][E].  A
+// thread takes 8 consecutive elements of its expert row and of its token row
+// and uses them as the k pairs of two MMAs: the order of a contraction is
+// free, as long as both operands share it.
+__device__ __forceinline__ void route_logits(const RouteParams& p, const RouteSplit& sp, float* part, int rank, int warp,
+                                             int lane) {
   const int g = lane >> 2, t4 = lane & 3;
   const int slice = (p.H + kRouteCtas * 32 - 1) / (kRouteCtas * 32) * 32;
-  const int k0 = min(p.H, rank * slice), k1 = min(p.H, k0 + slice);
+  const int sub = (slice / 32 + sp.ks - 1) / sp.ks * 32;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int e0 = warp * 16; e0 < p.E; e0 += kRouteWarps * 16) {
+  for (int u = warp; u < sp.et * sp.tg * sp.ks; u += kRouteWarps) {
+    const int e0 = u % sp.et * 16, n0 = u / sp.et % sp.tg * 32, ks = u / (sp.et * sp.tg);
+    const int end = min(p.H, (rank + 1) * slice);
+    const int k0 = min(end, rank * slice + ks * sub), k1 = min(end, k0 + sub);
     const bool r0 = e0 + g < p.E, r1 = e0 + g + 8 < p.E;
     const __nv_bfloat16* w0 = p.router + static_cast<int64_t>(e0 + g) * p.H;
     const __nv_bfloat16* w1 = w0 + static_cast<int64_t>(8) * p.H;
-    for (int n0 = 0; n0 < p.T; n0 += 32) {  // up to four token tiles of 8 at a time
-      float c[4][4] = {};
-      const int tiles = min(4, (p.T - n0 + 7) >> 3);
-#pragma unroll 4
-      for (int kk = k0 + t4 * 8; kk - t4 * 8 < k1; kk += 32) {
-        const bool in = kk < k1;
-        const uint4 a = (in && r0) ? __ldg(reinterpret_cast<const uint4*>(w0 + kk)) : zero;
-        const uint4 b = (in && r1) ? __ldg(reinterpret_cast<const uint4*>(w1 + kk)) : zero;
+    float c[4][4] = {};
+    const int tiles = min(4, (p.T - n0 + 7) >> 3);
+#pragma unroll 2
+    for (int kk = k0 + t4 * 8; kk - t4 * 8 < k1; kk += 32) {
+      const bool in = kk < k1;
+      const uint4 a = (in && r0) ? __ldg(reinterpret_cast<const uint4*>(w0 + kk)) : zero;
+      const uint4 b = (in && r1) ? __ldg(reinterpret_cast<const uint4*>(w1 + kk)) : zero;
+      uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j < tiles) {
-            const int t = n0 + j * 8 + g;
-            const uint4 v = (in && t < p.T)
-                                ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.H + kk))
-                                : zero;
-            mma_16816(c[j], a.x, b.x, a.y, b.y, v.x, v.y);
-            mma_16816(c[j], a.z, b.z, a.w, b.w, v.z, v.w);
-          }
-        }
+      for (int j = 0; j < 4; ++j) {
+        const int t = n0 + j * 8 + g;
+        v[j] = (in && t < p.T) ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.H + kk)) : zero;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int t = n0 + j * 8 + t4 * 2;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tt = t + (i & 1), e = e0 + g + (i >> 1) * 8;
-          if (j < tiles && tt < p.T && e < p.E) part[tt * p.E + e] = c[j][i];
+        if (j < tiles) {
+          mma_16816(c[j], a.x, b.x, a.y, b.y, v[j].x, v[j].y);
+          mma_16816(c[j], a.z, b.z, a.w, b.w, v[j].z, v[j].w);
         }
+      }
+    }
+    float* dst = part + ks * p.T * p.E;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = n0 + j * 8 + t4 * 2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tt = t + (i & 1), e = e0 + g + (i >> 1) * 8;
+        if (j < tiles && tt < p.T && e < p.E) dst[tt * p.E + e] = c[j][i];
       }
     }
   }
 }
 
-// One warp picks token t's experts.  Keys order by value, then by lower
-// index; a NaN orders last but stays a candidate, so that k valid experts
-// always come out (and the token's weights become NaN).
-__device__ __forceinline__ void route_pick(const RouteParams& p, const float* part, int t, int lane) {
+// One warp picks token t's experts, from the sums of all CTAs' parts, and
+// leaves them in the first CTA's s_idx too.  Keys order by value, equal ones
+// by the lower index; a NaN orders last but stays a candidate, so that k valid
+// experts always come out (and the token's weights become NaN).
+__device__ __forceinline__ void route_pick(const RouteParams& p, const float* part, const short* s_idx, int t,
+                                           int lane, bool skip) {
   constexpr int kPer = kMaxE / 32;
+  const int per = (p.E + 31) >> 5;
   float v[kPer];
   uint32_t key[kPer];
   float m = __int_as_float(0xff800000);
@@ -171,10 +202,13 @@ __device__ __forceinline__ void route_pick(const RouteParams& p, const float* pa
     const int e = lane + i * 32;
     v[i] = 0.0f;
     key[i] = 0u;
-    if (e < p.E) {
+    if (i < per && e < p.E) {
       const uint32_t at = smem_u32(part + t * p.E + e);
+      float f[kRouteCtas];
 #pragma unroll
-      for (int c = 0; c < kRouteCtas; ++c) v[i] += ld_cluster_f32(mapa_shared(at, c));
+      for (int c = 0; c < kRouteCtas; ++c) f[c] = ld_cluster_f32(mapa_shared(at, c));
+#pragma unroll
+      for (int c = 0; c < kRouteCtas; ++c) v[i] += f[c];
       m = fmaxf(m, v[i]);
       const uint32_t b = __float_as_uint(v[i] + 0.0f);  // -0 and 0 are equal
       key[i] = (v[i] != v[i]) ? 1u : ((b & 0x80000000u) ? ~b : (b | 0x80000000u));
@@ -185,104 +219,169 @@ __device__ __forceinline__ void route_pick(const RouteParams& p, const float* pa
   float z = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (lane + i * 32 < p.E) z += expf(v[i] - m);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  float mine = 0.0f, total = 0.0f;
+    if (i < per && lane + i * 32 < p.E) z += expf(v[i] - m);
+  z = route_sum(z);
+  float mine = 0.0f;
   int pick = 0;
   for (int n = 0; n < p.k; ++n) {
-    uint64_t best = 0;
+    uint32_t bk = 0u;
+    int be = 0;
     float bv = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (key[i] == 0u) continue;
-      const uint64_t c = (static_cast<uint64_t>(key[i]) << 32) | (0xffffffffu - (lane + i * 32));
-      if (c > best) {
-        best = c;
+    for (int i = 0; i < kPer; ++i)
+      if (i < per && key[i] > bk) {
+        bk = key[i];
+        be = lane + i * 32;
         bv = v[i];
       }
-    }
-    uint64_t top = best;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t u = __shfl_xor_sync(0xffffffffu, top, o);
-      top = u > top ? u : top;
-    }
-    const int src = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-    const float w = expf(__shfl_sync(0xffffffffu, bv, src) - m);
-    const int e = static_cast<int>(0xffffffffu - static_cast<uint32_t>(top));
+    const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+    const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, bk == top ? static_cast<uint32_t>(be) : 0xffffffffu));
+    const float l = __shfl_sync(0xffffffffu, bv, e & 31);  // the expert's own lane holds it
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (lane + i * 32 == e) key[i] = 0u;
-    total += w;
     if (lane == n) {
-      mine = w;
+      mine = expf(l - m);
       pick = e;
     }
   }
+  const float total = route_sum(mine);
   // z is NaN when any logit is: so are then the weights, renormalised or not
   const float denom = p.renorm ? (z == z ? total : z) : z;
   if (lane < p.k) {
-    p.idx[t * p.k + lane] = pick;
-    p.w[t * p.k + lane] = mine / denom;
+    if (!skip) {
+      p.idx[t * p.k + lane] = pick;
+      p.w[t * p.k + lane] = mine / denom;
+    }
+    st_cluster_u16(mapa_shared(smem_u32(s_idx + t * p.k + lane), 0), static_cast<uint16_t>(pick));
   }
 }
 
-__global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThreads)
+__global__ void __cluster_dims__(kRouteCtas, 1, 1) __maxnreg__(80)
     route_kernel(const RouteParams p) {
-  extern __shared__ float part[];  // [T][E] logits over this CTA's part of H
+  extern __shared__ float part[];  // logits over this CTA's part of H; then the first CTA's histograms
   __shared__ short s_idx[kMaxSlots];
   __shared__ int s_cnt[kMaxE + 1], s_act[kMaxE + 1], s_bad;
   const int rank = static_cast<int>(cluster_ctarank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_launch_dependents();  // experts_kernel may set itself up meanwhile
+  // A set status word only holds back the outputs: a CTA that left early would
+  // take its shared memory from the others.
   const bool skip = *reinterpret_cast<volatile int32_t*>(p.status) != 0;
-  if (skip) return;  // every CTA reads the same word: nobody writes it before the last barrier
   Plan* pl = p.plan;
+  const int S = p.T * p.k;
+  const bool few = p.T <= kRouteWarps;  // the first CTA picks for all tokens
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
   if (rank == kRouteCtas - 1) {
     for (int i = tid; i < kMaxE; i += kRouteThreads) pl->ready[i] = 0;
     for (int i = tid; i < kMaxCtas; i += kRouteThreads) pl->cut[i] = 0;
     if (tid == 0) pl->grid_bar = 0;
   }
   if (p.router != nullptr) {
-    route_logits(p, part, rank, warp, lane);
+    const RouteSplit sp = route_split(p.T, p.E);
+    route_logits(p, sp, part, rank, warp, lane);
+    if (sp.ks > 1) {
+      __syncthreads();
+      for (int i = tid; i < p.T * p.E; i += kRouteThreads) {
+        float v = part[i];
+        for (int k = 1; k < sp.ks; ++k) v += part[k * p.T * p.E + i];
+        part[i] = v;
+      }
+    }
     cluster_sync();
-    for (int t = rank + kRouteCtas * warp; t < p.T; t += kRouteCtas * kRouteWarps) route_pick(p, part, t, lane);
+    if (few) {
+      if (rank == 0 && warp < p.T) route_pick(p, part, s_idx, warp, lane, skip);
+    } else {
+      for (int t = rank + kRouteCtas * warp; t < p.T; t += kRouteCtas * kRouteWarps)
+        route_pick(p, part, s_idx, t, lane, skip);
+    }
+  } else if (rank == 0) {
+    for (int s = tid; s < S; s += kRouteThreads) {
+      const int e = p.idx[s];
+      const bool ok = e >= -1 && e < p.E;
+      if (!ok) s_bad = 1;
+      s_idx[s] = static_cast<short>(ok ? e : -1);
+    }
+    __syncthreads();
+    for (int t = tid; t < p.T; t += kRouteThreads)  // one expert twice for one token
+      for (int i = 1; i < p.k; ++i)
+        for (int j = 0; j < i; ++j)
+          if (s_idx[t * p.k + i] >= 0 && s_idx[t * p.k + i] == s_idx[t * p.k + j]) s_bad = 1;
   }
-  __threadfence();
-  cluster_sync();  // picks written; nobody reads this CTA's logits any more
-  if (rank != 0) return;
-  // sort the slots by expert (ascending), stable in the token
-  const int S = p.T * p.k;
-  if (tid == 0) s_bad = 0;
+  // The first CTA goes on once the picks are in its s_idx, the others leave
+  // once their logits have been read.
+  cluster_arrive();
+  if (rank != 0) {
+    cluster_wait();
+    return;
+  }
+  if (few) __syncthreads();
+  else cluster_wait();
+  if (S <= 32) {
+    // one warp holds all slots: positions by comparison with every other slot
+    if (warp == 0) {
+      const int e = lane < S ? s_idx[lane] : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, e);
+      const bool first = e >= 0 && (same & ((1u << lane) - 1)) == 0;
+      int pos = __popc(same & ((1u << lane) - 1)), j = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int ei = __shfl_sync(0xffffffffu, first ? e : -1, i);
+        const int ni = __popc(__shfl_sync(0xffffffffu, same, i));
+        if (ei >= 0 && ei < e) {
+          pos += ni;
+          ++j;
+        }
+      }
+      const int n_act = __popc(__ballot_sync(0xffffffffu, first)), n = __popc(__ballot_sync(0xffffffffu, e >= 0));
+      if (e >= 0) {
+        pl->slot_tok[pos] = lane / p.k;
+        pl->slot_act[pos] = j;
+        if (first) {
+          pl->act_e[j] = e;
+          pl->act_off[j] = pos;
+        }
+      }
+      if (lane < S) pl->pos_of[lane] = e >= 0 ? pos : -1;
+      if (lane == 0) {
+        pl->n_act = n_act;
+        pl->act_off[n_act] = n;
+        if (s_bad) atomicOr(p.status, GL_DEV_BAD_INDEX);
+      }
+    }
+    if (few) cluster_wait();
+    return;
+  }
+  // More: sort the slots by expert (ascending), stable in the token: a histogram
+  // per chunk of 32 slots, prefixes over the chunks and then over the experts.
+  uint16_t* hist = reinterpret_cast<uint16_t*>(part);  // [chunks][E]
+  const int chunks = (S + 31) >> 5;
+  for (int i = tid; i < chunks * p.E; i += kRouteThreads) hist[i] = 0;
   __syncthreads();
-  for (int s = tid; s < S; s += kRouteThreads) {
-    const int e = __ldcg(p.idx + s);
-    if (e < -1 || e >= p.E) s_bad = 1;
-    s_idx[s] = static_cast<short>((e < 0 || e >= p.E) ? -1 : e);
-    pl->pos_of[s] = -1;
+  for (int c = warp; c < chunks; c += kRouteWarps) {
+    const int s = c * 32 + lane;
+    const int e = s < S ? s_idx[s] : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && (same & ((1u << lane) - 1)) == 0) hist[c * p.E + e] = static_cast<uint16_t>(__popc(same));
   }
   __syncthreads();
   int cnt = 0;
-  if (tid < p.E) {
-    int last = -1;
-    for (int s = 0; s < S; ++s) {
-      if (s_idx[s] == tid) {
-        const int t = s / p.k;
-        if (t == last) s_bad = 1;  // one expert twice for one token
-        last = t;
-        ++cnt;
-      }
-    }
-  }
   if (tid < kMaxE) {
+    if (tid < p.E)
+      for (int c = 0; c < chunks; ++c) {
+        const int h = hist[c * p.E + tid];
+        hist[c * p.E + tid] = static_cast<uint16_t>(cnt);
+        cnt += h;
+      }
     s_cnt[tid] = cnt;
     s_act[tid] = cnt > 0;
   }
   __syncthreads();
-  // exclusive scans of the counts and of the active flags (E <= 256: one warp, 8 a lane)
-  if (warp == 0) {
+  if (warp == 0) {  // exclusive scans of the counts and of the active flags, 8 experts a lane
     constexpr int kPer = kMaxE / 32;
     int c = 0, a = 0;
+#pragma unroll
     for (int i = 0; i < kPer; ++i) {
       c += s_cnt[lane * kPer + i];
       a += s_act[lane * kPer + i];
@@ -298,6 +397,7 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
     }
     c = ci - c;
     a = ai - a;
+#pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int nc = s_cnt[lane * kPer + i], na = s_act[lane * kPer + i];
       s_cnt[lane * kPer + i] = c;
@@ -312,29 +412,42 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
   }
   __syncthreads();
   if (tid < p.E && cnt > 0) {
-    int pos = s_cnt[tid];
-    const int j = s_act[tid];
-    pl->act_e[j] = tid;
-    pl->act_off[j] = pos;
-    for (int s = 0; s < S; ++s)
-      if (s_idx[s] == tid) {
+    pl->act_e[s_act[tid]] = tid;
+    pl->act_off[s_act[tid]] = s_cnt[tid];
+  }
+  for (int c = warp; c < chunks; c += kRouteWarps) {
+    const int s = c * 32 + lane;
+    const int e = s < S ? s_idx[s] : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (s < S) {
+      int pos = -1;
+      if (e >= 0) {
+        pos = s_cnt[e] + hist[c * p.E + e] + __popc(same & ((1u << lane) - 1));
         pl->slot_tok[pos] = s / p.k;
-        pl->slot_act[pos] = j;
-        pl->pos_of[s] = pos++;
+        pl->slot_act[pos] = s_act[e];
       }
+      pl->pos_of[s] = pos;
+    }
   }
   if (tid == 0) {
     pl->n_act = s_act[kMaxE];
     pl->act_off[s_act[kMaxE]] = s_cnt[kMaxE];
     if (s_bad) atomicOr(p.status, GL_DEV_BAD_INDEX);
   }
+  if (few) cluster_wait();
+}
+
+// Dynamic shared memory of route_kernel.
+int route_smem(int T, int E, int k, bool router) {
+  const int hist = (T * k + 31) / 32 * E * 2;
+  return std::max(hist, router ? route_split(T, E).ks * T * E * 4 : 0);
 }
 
 // ------------------------------------------------------------------- experts
 constexpr int kThreads = 256;  // warps: 0 weights, 1 tokens / h, 2 MMA, 3 -, 4-7 epilogue
 constexpr int kABytes = 128 * 64 * 2;
 constexpr int kChunk = 16;     // slots per epilogue step
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 11;
 constexpr int kBarBytes = 256;
 constexpr int kExBytes = kChunk * 64 * 4;
 
@@ -374,24 +487,36 @@ struct ExpertMaps<false> {
 };
 
 // One phase's list of blocks: unit u = (active expert, tile) has `kb` blocks;
-// CTA c takes the blocks [c total / ctas, (c + 1) total / ctas).
+// of the list's grains of `grain` blocks (one, or a whole tile's) CTA c takes
+// [c total / ctas, (c + 1) total / ctas).
 struct Phase {
   int tiles;      // tiles per expert
   int kb;         // blocks per tile
-  int64_t total;  // blocks
+  int grain;      // blocks that stay together
+  int64_t total;  // grains
   int ctas;       // CTAs with work
-  __device__ int64_t begin(int c) const { return total * c / ctas; }
+  __device__ int64_t begin(int c) const { return total * c / ctas * grain; }
   // the CTA that takes block b
-  __device__ int owner(int64_t b) const { return static_cast<int>(((b + 1) * ctas - 1) / total); }
+  __device__ int owner(int64_t b) const { return static_cast<int>(((b / grain + 1) * ctas - 1) / total); }
 };
 
-__device__ __forceinline__ Phase make_phase(int n_act, int tiles, int kb, int ctas) {
+__device__ __forceinline__ Phase make_phase(int n_act, int tiles, int kb, int ctas, bool whole) {
   Phase f;
   f.tiles = tiles;
   f.kb = kb;
-  f.total = static_cast<int64_t>(n_act) * tiles * kb;
+  f.grain = whole ? kb : 1;
+  f.total = static_cast<int64_t>(n_act) * tiles * (whole ? 1 : kb);
   f.ctas = static_cast<int>(f.total < ctas ? f.total : ctas);
   return f;
+}
+
+// Whether the W1 tiles are better left whole: the slowest CTA's extra blocks
+// against the exchange of a cut tile's partials (two trips through L2 and an
+// atomic, about as long as kCutBlocks blocks take to stream).
+constexpr int kCutBlocks = 8;
+__device__ __forceinline__ bool keep_whole(int units, int kb, int ctas) {
+  const int64_t most = static_cast<int64_t>((units + ctas - 1) / ctas) * kb;
+  return most <= static_cast<int64_t>(units) * kb / ctas + kCutBlocks;
 }
 
 // Blocks [lo, hi) of one tile: what a CTA accumulates at a time.
@@ -433,6 +558,13 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+// A release by one thread after a barrier covers the writes of all the
+// barrier's threads, an acquire before one their reads.
+__device__ __forceinline__ int atom_acq_rel_add1(int* p) {
+  int v;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ void red_release_add1(int* p) {
   asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
 }
@@ -449,6 +581,10 @@ __device__ __forceinline__ bool wait_count(const int* p, int want, const volatil
     if (*abort) return false;
     if (globaltimer_ns() - t0 > limit_ns) return false;
   }
+}
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
 __device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -490,12 +626,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = static_cast<int>(blockIdx.x);
-  if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
-  const int n_act = p.plan->n_act;
-  for (int i = tid; i < n_act; i += kThreads) act_e[i] = p.plan->act_e[i];
-  for (int i = tid; i <= n_act; i += kThreads) act_off[i] = p.plan->act_off[i];
-  const int S = n_act > 0 ? p.plan->act_off[n_act] : 0;
-  for (int i = tid; i < S; i += kThreads) slot_tok[i] = static_cast<uint8_t>(p.plan->slot_tok[i]);
+  if (warp == 3 && lane == 0) {
+    tma_prefetch_desc(&p.x);
+    tma_prefetch_desc(&p.h);
+    if (!PG) {
+      tma_prefetch_desc(&p.w1);
+      tma_prefetch_desc(&p.w2);
+    }
+  }
   if (tid == 0) {
     *abort_flag = 0;
     for (int s = 0; s < p.stages; ++s) {
@@ -513,13 +651,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, 256);  // two 128 x 128 fp32 accumulators
     tmem_relinquish();
   }
+  grid_dependency_wait();  // route_kernel's results from here on
+  // the plan: all of it at once, whatever part is in use, so that its loads overlap
+  const int status = *reinterpret_cast<volatile int32_t*>(p.status);
+  const int n_act = p.plan->n_act;
+  static_assert(kThreads == kMaxE, "one expert a thread");
+  act_e[tid] = p.plan->act_e[tid];
+  act_off[tid] = p.plan->act_off[tid];
+  if (tid == 0) act_off[kMaxE] = p.plan->act_off[kMaxE];
+  for (int i = tid; i < p.T * p.k; i += kThreads) slot_tok[i] = static_cast<uint8_t>(p.plan->slot_tok[i]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if (status != 0) {
+    if (warp == 2) tmem_dealloc(tmem_base, 256);
+    return;
+  }
   const int ctas = static_cast<int>(gridDim.x);
-  const Phase f1 = make_phase(n_act, (p.F + 63) / 64, (p.H + 63) / 64, ctas);
-  const Phase f2 = make_phase(n_act, (p.H + 127) / 128, (p.F + 63) / 64, ctas);
+  const int tiles1 = (p.F + 63) / 64, kb1 = (p.H + 63) / 64;
+  const Phase f1 = make_phase(n_act, tiles1, kb1, ctas, keep_whole(n_act * tiles1, kb1, ctas));
+  const Phase f2 = make_phase(n_act, (p.H + 127) / 128, (p.F + 63) / 64, ctas, false);
 
   // Before a producer leaves: wait for its last copies to land (the stage also
   // waits for the other producer, which may have given up: one bound for all).
@@ -714,12 +866,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole) {
         // the last CTA to arrive at a cut tile adds the partials, in CTA order
         const int c0 = f1.owner(s.first), c1 = f1.owner(s.first + f1.kb - 1);
-        __threadfence();
         bar_epilogue();
-        if (et == 0) *flag = atomicAdd(&p.plan->cut[c0], 1) == c1 - c0;
+        if (et == 0) *flag = atom_acq_rel_add1(&p.plan->cut[c0]) == c1 - c0;
         bar_epilogue();
         if (!*flag) return true;
-        __threadfence();
         const int r64 = et & 63;
         for (int i = et >> 6; i < n; i += 2) {
           float u0 = 0.0f, u1 = 0.0f;
@@ -734,7 +884,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // h is read by other CTAs' TMA
       fence_proxy_async_all();
-      __threadfence();
       bar_epilogue();
       if (et == 0) red_release_add1(&p.plan->ready[s.j]);
       return true;
@@ -775,70 +924,93 @@ __global__ void __launch_bounds__(kThreads, 1)
       });
   }
 
-  __threadfence();
   tc_fence_before();
   __syncthreads();
+  // ===================== weighted sum =====================
+  // An item is 128 columns of 8 / wpt tokens: wpt warps share a token's choices
+  // (few tokens would leave warps idle and chain the loads of all choices in
+  // one).  Lane i holds the token's choice i: its slot, the slot's row in a
+  // partial, the CTAs that its tile is cut between, its weight.  (The first
+  // ones are looked up before the barrier.)
+  struct Choice {
+    int pos, s, c0, c1;
+    float w;
+  };
+  const int wpt = p.T == 1 ? 8 : p.T == 2 ? 4 : p.T <= 4 ? 2 : 1;
+  const int tpi = 8 / wpt, sub = warp % wpt;
+  const int tiles = f2.tiles, items = tiles * ((p.T + tpi - 1) / tpi);
+  auto look_up = [&](int item) {
+    Choice c{-1, 0, 0, 0, 0.0f};
+    const int tile = item % tiles, t = item / tiles * tpi + warp / wpt;
+    if (item < items && t < p.T && lane < p.k) {
+      c.pos = p.plan->pos_of[t * p.k + lane];
+      c.w = p.w[t * p.k + lane];
+      if (c.pos >= 0) {
+        const int j = p.plan->slot_act[c.pos];
+        const int64_t first = (static_cast<int64_t>(j) * tiles + tile) * f2.kb;
+        c.s = c.pos - act_off[j];
+        c.c0 = f2.owner(first);
+        c.c1 = f2.owner(first + f2.kb - 1);
+      }
+    }
+    return c;
+  };
+  if (tid == 0 && !*abort_flag) red_release_add1(&p.plan->grid_bar);
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem_base, 256);
   }
-  // ===================== weighted sum =====================
+  Choice ch = look_up(cta);
   if (tid == 0) {
-    bool all = !*abort_flag;
-    if (all) {
-      red_release_add1(&p.plan->grid_bar);
-      all = wait_count(&p.plan->grid_bar, ctas, abort_flag, p.wait_ns);
-      if (!all) report_abort(abort_flag, p.status);
-    }
+    const bool all = !*abort_flag && wait_count(&p.plan->grid_bar, ctas, abort_flag, p.wait_ns);
+    if (!all) report_abort(abort_flag, p.status);
     *flag = all;
   }
   __syncthreads();
   if (!*flag) return;
-  const int tiles = f2.tiles, groups = (p.T + 7) / 8;
-  for (int item = cta; item < tiles * groups; item += ctas) {
-    const int tile = item % tiles, t = item / tiles * 8 + warp;  // a warp per token, four columns a lane
+  for (int item = cta; item < items; item += ctas) {
+    const int tile = item % tiles, t = item / tiles * tpi + warp / wpt;
     const int col = tile * 128 + lane * 4;
-    if (t >= p.T) continue;
-    int pos = -1, s = 0, c0 = 0, c1 = 0;
-    float w = 0.0f;
-    if (lane < p.k) {
-      pos = p.plan->pos_of[t * p.k + lane];
-      w = __ldcg(p.w + t * p.k + lane);
-      if (pos >= 0) {
-        const int j = p.plan->slot_act[pos];
-        const int64_t first = (static_cast<int64_t>(j) * tiles + tile) * f2.kb;
-        s = pos - act_off[j];
-        c0 = f2.owner(first);
-        c1 = f2.owner(first + f2.kb - 1);
-      }
-    }
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = 0; i < p.k; ++i) {
-      const int pi = __shfl_sync(0xffffffffu, pos, i), si = __shfl_sync(0xffffffffu, s, i);
-      const int b = __shfl_sync(0xffffffffu, c0, i), e = __shfl_sync(0xffffffffu, c1, i);
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      if (pi < 0 || col >= p.H) continue;
-      float4 v = __ldcg(reinterpret_cast<const float4*>(p.pbuf + static_cast<int64_t>(pi) * p.H + col));
-      for (int c = b + 1; c <= e; ++c) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(
-            p.part2 + (static_cast<int64_t>(c) * p.nt + si) * 128 + lane * 4));
-        v.x += a.x;
-        v.y += a.y;
-        v.z += a.z;
-        v.w += a.w;
+    if (t < p.T) {
+#pragma unroll 4
+      for (int i = sub; i < p.k; i += wpt) {
+        const int pi = __shfl_sync(0xffffffffu, ch.pos, i), si = __shfl_sync(0xffffffffu, ch.s, i);
+        const int b = __shfl_sync(0xffffffffu, ch.c0, i), e = __shfl_sync(0xffffffffu, ch.c1, i);
+        const float wi = __shfl_sync(0xffffffffu, ch.w, i);
+        const bool in = pi >= 0 && col < p.H;
+        // the tile's first segment, and the partials of up to two more CTAs at once
+        const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float* more = p.part2 + (static_cast<int64_t>(b) * p.nt + si) * 128 + lane * 4;
+        const int64_t pitch = static_cast<int64_t>(p.nt) * 128;
+        float4 v = in ? __ldcg(reinterpret_cast<const float4*>(p.pbuf + static_cast<int64_t>(pi) * p.H + col)) : zero;
+        const float4 a1 = in && b + 1 <= e ? __ldcg(reinterpret_cast<const float4*>(more + pitch)) : zero;
+        const float4 a2 = in && b + 2 <= e ? __ldcg(reinterpret_cast<const float4*>(more + 2 * pitch)) : zero;
+        v = add4(add4(v, a1), a2);
+        if (in)
+          for (int c = b + 3; c <= e; ++c) v = add4(v, __ldcg(reinterpret_cast<const float4*>(more + (c - b) * pitch)));
+        sum.x = fmaf(wi, v.x, sum.x);
+        sum.y = fmaf(wi, v.y, sum.y);
+        sum.z = fmaf(wi, v.z, sum.z);
+        sum.w = fmaf(wi, v.w, sum.w);
       }
-      sum.x = fmaf(wi, v.x, sum.x);
-      sum.y = fmaf(wi, v.y, sum.y);
-      sum.z = fmaf(wi, v.z, sum.z);
-      sum.w = fmaf(wi, v.w, sum.w);
     }
-    if (col < p.H) {  // H % 8 == 0: four columns are all in or all out
+    if (wpt > 1) {  // add the shares of the token's warps, in order
+      float4* share = reinterpret_cast<float4*>(ex);
+      __syncthreads();
+      share[warp * 32 + lane] = sum;
+      __syncthreads();
+      if (sub == 0)
+        for (int i = 1; i < wpt; ++i) sum = add4(sum, share[(warp + i) * 32 + lane]);
+    }
+    if (sub == 0 && t < p.T && col < p.H) {  // H % 8 == 0: four columns are all in or all out
       __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y), hi = __floats2bfloat162_rn(sum.z, sum.w);
       uint2 o;
       o.x = *reinterpret_cast<uint32_t*>(&lo);
       o.y = *reinterpret_cast<uint32_t*>(&hi);
       *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(t) * p.H + col) = o;
     }
+    if (item + ctas < items) ch = look_up(item + ctas);
   }
 }
 
@@ -861,11 +1033,13 @@ gl_status launch_experts(const ExpertParams& prm, const ExpertMaps<PG>& pg, int 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait for one another: all resident, or none
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, prm, pg) == cudaSuccess ? GL_OK : GL_ERR_CUDA;
 }
 
@@ -933,7 +1107,7 @@ gl_status launch_moe(const MoeCall& c) {
   }
   gl_status st = ok ? GL_OK : GL_ERR_UNSUPPORTED;
   if (ok) {
-    const int rsmem = c.router != nullptr ? c.T * c.E * 4 : 0;
+    const int rsmem = route_smem(c.T, c.E, c.k, c.router != nullptr);
     if (set_max_smem(reinterpret_cast<const void*>(route_kernel), kMaxT * kMaxE * 4) != cudaSuccess) {
       st = GL_ERR_CUDA;
     } else {

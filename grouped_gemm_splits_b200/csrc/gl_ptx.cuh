@@ -474,3 +474,21 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* t
 }
 
 }  // namespace gl
+
+namespace gl {
+
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- dependent launches
+// Let the next kernel of the stream start (it was launched to wait for this
+// one's results with grid_dependency_wait).
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Until the kernel before has finished and its writes are visible; nothing to
+// wait for in an ordinary launch.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+}  // namespace gl

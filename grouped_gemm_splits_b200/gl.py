@@ -413,38 +413,51 @@ def gl_wgrad_mxfp8(x_codes_c: torch.Tensor, x_scales_c: torch.Tensor, dy_codes_c
 
 # ------------------------------------------------------------------- RMS norm
 
-def _need(ok: bool, what: str, why: str) -> None:
-    if not ok:
-        raise GlError(f"{what}: {why}")
+def _refuse(what: str, why: str) -> None:
+    raise GlError(f"{what}: {why}")
 
 
 def _tensor(what: str, name: str, t, dtype, *shapes) -> None:
     """Refuse anything but a contiguous tensor of this dtype and one of these shapes."""
-    _need(isinstance(t, torch.Tensor), what, f"{name} must be a tensor")
-    _need(t.dtype == dtype, what, f"{name} must be {dtype}, not {t.dtype}")
-    _need(tuple(t.shape) in shapes, what, f"{name} must be {' or '.join(map(str, shapes))}, not {tuple(t.shape)}")
-    _need(t.is_contiguous(), what, f"{name} must be contiguous")
+    if not isinstance(t, torch.Tensor):
+        _refuse(what, f"{name} must be a tensor")
+    if t.dtype is not dtype:
+        _refuse(what, f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape not in shapes:
+        _refuse(what, f"{name} must be {' or '.join(map(str, shapes))}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        _refuse(what, f"{name} must be contiguous")
+
+
+def _matrix(what: str, name: str, t) -> torch.Size:
+    """The shape of a contiguous bf16 [rows, cols] tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        _refuse(what, f"{name} must be a matrix")
+    _tensor(what, name, t, torch.bfloat16, t.shape)
+    return t.shape
 
 
 class _On:
     """The device of a call's tensors, made current for the call; yields its current stream."""
 
-    def __init__(self, what: str, *tensors):
-        dev = tensors[0].device
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise GlError(f"{what}: tensors on {dev} and {t.device}")
-        _need(dev.type == "cuda", what, f"tensors must be on a CUDA device, not {dev}")
-        self.dev = dev
+    __slots__ = ("dev", "old")
 
-    def __enter__(self):
+    def __init__(self, what: str, first: torch.Tensor, *others):
+        self.dev = first.get_device()
+        for t in others:
+            if t is not None and t.get_device() != self.dev:
+                _refuse(what, f"tensors on {first.device} and {t.device}")
+        if self.dev < 0:
+            _refuse(what, f"tensors must be on a CUDA device, not {first.device}")
+
+    def __enter__(self) -> int:
         self.old = torch.cuda.current_device()
-        if self.old != self.dev.index:
+        if self.old != self.dev:
             torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream(self.dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.dev)
 
     def __exit__(self, *exc):
-        if self.old != self.dev.index:
+        if self.old != self.dev:
             torch.cuda.set_device(self.old)
 
 
@@ -461,36 +474,41 @@ def gl_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optio
     """
     what = "gl_rmsnorm"
     bf = torch.bfloat16
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, what, "x must be a [rows, cols] tensor")
-    rows, cols = x.shape
-    _tensor(what, "x", x, bf, (rows, cols))
+    shape = _matrix(what, "x", x)
+    rows, cols = shape
     _tensor(what, "gamma", gamma, bf, (cols,))
     if residual is not None:
-        _tensor(what, "residual", residual, bf, (rows, cols))
-    _need(y or mxfp8, what, "at least one of y and mxfp8 is required")
-    if mxfp8:
-        _need(cols % (128 if mma_scales else 32) == 0, what, f"cols = {cols} does not fit the scale layout")
-    out = {} if out is None else dict(out)
-    want = {"rstd": (torch.float32, (rows,))}
-    if residual is not None or "sum" in out:
-        want["sum"] = (bf, (rows, cols))
+        _tensor(what, "residual", residual, bf, shape)
+    if not (y or mxfp8):
+        _refuse(what, "at least one of y and mxfp8 is required")
+    if mxfp8 and cols % (128 if mma_scales else 32):
+        _refuse(what, f"cols = {cols} does not fit the scale layout")
+    given = out
+    want = [("rstd", torch.float32, (rows,))]
+    if residual is not None or (given and "sum" in given):
+        want.append(("sum", bf, shape))
     if y:
-        want["y"] = (bf, (rows, cols))
+        want.append(("y", bf, shape))
     if mxfp8:
-        want["codes_r"] = (torch.uint8, (rows, cols))
-        want["scales_r"] = (torch.uint8, ((mxfp8_scale_bytes(rows, cols, 1, False, True) if rows else 0,)
-                                          if mma_scales else (rows, cols // 32)))
-    for key, t in out.items():
-        _need(key in want, what, f"out[{key!r}] is not an output of this call")
-        dt, shape = want[key]
-        if key == "scales_r":
-            _tensor(what, key, t, dt, shape, (rows * (cols // 32),) if not mma_scales else shape)
-        else:
-            _tensor(what, key, t, dt, shape)
-    with _On(what, x, gamma, residual, *out.values()) as stream:
-        for key, (dt, shape) in want.items():
-            if key not in out:
-                out[key] = torch.empty(shape, dtype=dt, device=x.device)
+        want.append(("codes_r", torch.uint8, shape))
+        want.append(("scales_r", torch.uint8, ((rows + 127) // 128 * (cols // 128) * 512,) if mma_scales
+                     else (rows, cols // 32)))
+    out = {}
+    if given:
+        names = [w[0] for w in want]
+        for key in given:
+            if key not in names:
+                _refuse(what, f"out[{key!r}] is not an output of this call")
+    with _On(what, x, gamma, residual, *(given.values() if given else ())) as stream:
+        for key, dt, sh in want:
+            t = given.get(key) if given else None
+            if t is None:
+                t = torch.empty(sh, dtype=dt, device=x.device)
+            elif key == "scales_r":
+                _tensor(what, key, t, dt, sh, (rows * (cols // 32),) if not mma_scales else sh)
+            else:
+                _tensor(what, key, t, dt, sh)
+            out[key] = t
         _check(load().gl_rmsnorm(x.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, rows, cols,
                                  _ptr(out.get("sum")), _ptr(out.get("y")), out["rstd"].data_ptr(),
                                  _ptr(out.get("codes_r")), _ptr(out.get("scales_r")),
@@ -518,9 +536,7 @@ def gl_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, gamma: torch.Tensor, rst
     """
     what = "gl_rmsnorm_bwd"
     bf = torch.bfloat16
-    _need(isinstance(dy, torch.Tensor) and dy.dim() == 2, what, "dy must be a [rows, cols] tensor")
-    rows, cols = dy.shape
-    _tensor(what, "dy", dy, bf, (rows, cols))
+    rows, cols = _matrix(what, "dy", dy)
     _tensor(what, "sum", sum, bf, (rows, cols))
     _tensor(what, "gamma", gamma, bf, (cols,))
     _tensor(what, "rstd", rstd, torch.float32, (rows,))
@@ -530,7 +546,8 @@ def gl_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, gamma: torch.Tensor, rst
         _tensor(what, "dx", dx, bf, (rows, cols))
     if dgamma is not None:
         _tensor(what, "dgamma", dgamma, torch.float32, (cols,))
-    _need(dgamma is not None or not accumulate, what, "accumulate needs a dgamma")
+    if accumulate and dgamma is None:
+        _refuse(what, "accumulate needs a dgamma")
     with _On(what, dy, sum, gamma, rstd, dsum, dx, dgamma, workspace) as stream:
         if dx is None:
             dx = torch.empty(rows, cols, dtype=bf, device=dy.device)
@@ -555,24 +572,26 @@ def _weights(what: str, name: str, w: TensorOrList, G: int, *shapes) -> torch.Te
     if isinstance(w, torch.Tensor):
         _tensor(what, name, w, torch.bfloat16, *[(G, *s) for s in shapes])
         return w
-    _need(len(w) == G, what, f"{name} must have {G} tensors, not {len(w)}")
+    if len(w) != G:
+        _refuse(what, f"{name} must have {G} tensors, not {len(w)}")
     for t in w:
         _tensor(what, name, t, torch.bfloat16, *shapes)
-        _need(t.device == w[0].device, what, f"{name} on {w[0].device} and {t.device}")
+        if t.device != w[0].device:
+            _refuse(what, f"{name} on {w[0].device} and {t.device}")
     return w[0]
 
 
 def _plan(what: str, offsets: torch.Tensor, status: torch.Tensor) -> int:
-    _need(isinstance(offsets, torch.Tensor) and offsets.dim() == 1 and offsets.numel() >= 2, what,
-          "offsets must be the [G + 1] tensor of gl_offsets")
-    _tensor(what, "offsets", offsets, torch.int64, tuple(offsets.shape))
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        _refuse(what, "offsets must be the [G + 1] tensor of gl_offsets")
+    _tensor(what, "offsets", offsets, torch.int64, offsets.shape)
     _tensor(what, "status", status, torch.int32, (1,), ())
     return offsets.numel() - 1
 
 
 def _rows_at_least(what: str, name: str, t: torch.Tensor, rows: int, cols: int) -> None:
-    _need(isinstance(t, torch.Tensor) and t.dim() == 2 and t.shape[0] >= rows, what,
-          f"{name} must have at least {rows} rows")
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] < rows:
+        _refuse(what, f"{name} must have at least {rows} rows")
     _tensor(what, name, t, torch.bfloat16, (t.shape[0], cols))
 
 
@@ -588,12 +607,12 @@ def gl_fwd_act(x: torch.Tensor, w: TensorOrList, bias: Optional[TensorOrList], o
     """
     what = "gl_fwd_act"
     G = _plan(what, offsets, status)
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, what, "x must be a [rows, K] tensor")
-    M, K = x.shape
-    _tensor(what, "x", x, torch.bfloat16, (M, K))
-    _need(act in ACTS.values(), what, f"unknown activation {act}")
+    M, K = _matrix(what, "x", x)
+    if not GL_ACT_NONE <= act <= GL_ACT_GEGLU:
+        _refuse(what, f"unknown activation {act}")
     N = _shape_nk(w)[0]
-    _need(not _gated(act) or N % 2 == 0, what, f"a gated activation halves {N} columns")
+    if _gated(act) and N % 2:
+        _refuse(what, f"a gated activation halves {N} columns")
     w0 = _weights(what, "w", w, G, (N, K))
     b0 = _weights(what, "bias", bias, G, (N,)) if bias is not None else None
     Nout = N // 2 if _gated(act) else N
@@ -629,10 +648,9 @@ def gl_dgrad_act(dy: torch.Tensor, w: TensorOrList, z: torch.Tensor, offsets: to
     gradients)."""
     what = "gl_dgrad_act"
     G = _plan(what, offsets, status)
-    _need(isinstance(dy, torch.Tensor) and dy.dim() == 2, what, "dy must be a [rows, N] tensor")
-    M, N = dy.shape
-    _tensor(what, "dy", dy, torch.bfloat16, (M, N))
-    _need(act in ACTS.values() and act != GL_ACT_NONE, what, f"activation {act} has no slope to apply")
+    M, N = _matrix(what, "dy", dy)
+    if not GL_ACT_NONE < act <= GL_ACT_GEGLU:
+        _refuse(what, f"activation {act} has no slope to apply")
     K = _shape_nk(w)[1]
     w0 = _weights(what, "w", w, G, (N, K))
     width = 2 * K if _gated(act) else K
@@ -677,19 +695,18 @@ def gl_moe_tokens(x: torch.Tensor, w1: TensorOrList, w2: TensorOrList, top_k: in
     """
     what = "gl_moe_tokens"
     bf = torch.bfloat16
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, what, "x must be a [tokens, H] tensor")
-    T, H = x.shape
-    _tensor(what, "x", x, bf, (T, H))
+    T, H = _matrix(what, "x", x)
     _tensor(what, "status", status, torch.int32, (1,), ())
     E = len(w1)
     F = _shape_nk(w2)[1]
     a = _weights(what, "w1", w1, E, (2 * F, H))
     b = _weights(what, "w2", w2, E, (H, F))
-    _need(T <= GL_MOE_MAX_TOKENS, what, f"{T} tokens: at most {GL_MOE_MAX_TOKENS}")
+    if T > GL_MOE_MAX_TOKENS:
+        _refuse(what, f"{T} tokens: at most {GL_MOE_MAX_TOKENS}")
     if router_w is not None:
         _tensor(what, "router_w", router_w, bf, (E, H))
-    else:
-        _need(topk_idx is not None and topk_w is not None, what, "router_w, or topk_idx and topk_w, are required")
+    elif topk_idx is None or topk_w is None:
+        _refuse(what, "router_w, or topk_idx and topk_w, are required")
     if topk_idx is not None:
         _tensor(what, "topk_idx", topk_idx, torch.int32, (T, top_k))
     if topk_w is not None:
