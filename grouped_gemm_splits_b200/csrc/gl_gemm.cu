@@ -67,7 +67,7 @@ __host__ __device__ constexpr int band_rows() { return MODE == kFwd ? 16 : 8; }
 // Epilogue forms of FWD and DGRAD.
 enum { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2 };
 
-template <int MODE, int CG>
+template <int MODE, int CG, int EPI = kEpiPlain>
 struct Cfg {
   static constexpr int kTileM = 128 * CG;          // accumulator rows per tile (pair)
   static constexpr int kTileN = 256;               // accumulator columns
@@ -83,8 +83,9 @@ struct Cfg {
   static constexpr int kBBytes = kBRows * kBK * 2;  // 32 KB
   static constexpr int kStageBytes = kABytes + kBBytes;
   // epilogue warps, one per TMEM lane quarter (eight for wgrad measured no
-  // faster and cost a pipeline stage of staging space)
-  static constexpr int kEpiWarps = 4;
+  // faster and cost a pipeline stage of staging space); two per quarter for the
+  // activation forms, whose epilogue is longer than a K = 2048 main loop with one
+  static constexpr int kEpiWarps = EPI == kEpiPlain ? 4 : 8;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kStagingBytes = (MODE == kWgrad) ? kEpiWarps * 32 * 32 * 4 : 0;  // one 4 KB transpose per epilogue warp
   static constexpr int kStages = (kSmemBudget - kStagingBytes) / kStageBytes;
@@ -243,10 +244,8 @@ __device__ __forceinline__ void zero_tail_rows(uint8_t* sa, uint8_t* sb, int r_f
   fence_proxy_async_smem();
 }
 
-// Eight consecutive bf16 values as fp32 (plain loads: y may be the residual's
-// buffer).
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+// Eight bf16 values as fp32.
+__device__ __forceinline__ void unpack8(const uint4& w, float* v) {
   const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(&w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = __bfloat162float(b[j]);
@@ -268,26 +267,39 @@ __device__ __forceinline__ void load_acc32(uint32_t taddr, uint32_t (&r)[32]) {
   tmem_reg_fence(r);
 }
 
-// One thread's part of a tile in the forms kEpiAct / kEpiGated: its row's
-// columns [n0, n0 + out_tile), 32 at a time.  `release` is called once the
-// accumulator has been read.
+// One thread's part of a tile in the forms kEpiAct / kEpiGated: every other
+// chunk of 32 of its row's columns [n0, n0 + out_tile), from chunk `half` on.
+// What a chunk reads from global memory is asked for before its accumulator
+// columns.  `release` is called once the accumulator has been read.
 template <int MODE, int EPI, typename Release>
 __device__ __forceinline__ void epilogue_act(const GemmParams& p, uint32_t tacc, int64_t row, bool row_ok, int n0,
-                                             const __nv_bfloat16* bias, Release release) {
+                                             int half, const __nv_bfloat16* bias, Release release) {
   constexpr int kOut = out_tile<MODE, EPI>();
+  constexpr bool kFwdGated = EPI == kEpiGated && MODE == kFwd, kBwdGated = EPI == kEpiGated && MODE == kDgrad;
   const int F = out_cols<MODE, EPI>(p);  // columns of y (FWD) or of dy W (DGRAD)
-  const int width = (EPI == kEpiGated && MODE == kDgrad) ? 2 * F : F;
+  const int width = kBwdGated ? 2 * F : F;
   const int64_t zw = (MODE == kFwd) ? p.N : width;  // columns of z
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + row * width;
   __nv_bfloat16* z = p.z + row * zw;
-  const __nv_bfloat16* res = p.residual + row * F;
+  // read per chunk: the residual (FWD) or z (DGRAD), and z's second half
+  const __nv_bfloat16* src = (MODE == kFwd) ? p.residual + row * F : z;
+  const bool reads = row_ok && (MODE == kDgrad || p.residual != nullptr);
   const int nchunks = min(kOut / 32, ceil_div_i(F - n0, 32));
-  for (int c = 0; c < nchunks; ++c) {
+  if (half >= nchunks) release();  // this warp's chunks lie past the last column
+  for (int c = half; c < nchunks; c += 2) {
     const int n = n0 + c * 32;
-    uint32_t r[32], r1[EPI == kEpiGated && MODE == kFwd ? 32 : 1];
+    uint4 g0[4], g1[kBwdGated ? 4 : 1];
+#pragma unroll
+    for (int j8 = 0; j8 < 4; ++j8) {
+      if (reads && n + j8 * 8 < F) {
+        g0[j8] = *reinterpret_cast<const uint4*>(src + n + j8 * 8);
+        if constexpr (kBwdGated) g1[j8] = *reinterpret_cast<const uint4*>(src + F + n + j8 * 8);
+      }
+    }
+    uint32_t r[32], r1[kFwdGated ? 32 : 1];
     load_acc32(tacc + c * 32, r);
-    if constexpr (EPI == kEpiGated && MODE == kFwd) load_acc32(tacc + kOut + c * 32, r1);
-    if (c == nchunks - 1) release();
+    if constexpr (kFwdGated) load_acc32(tacc + kOut + c * 32, r1);
+    if (c + 2 >= nchunks) release();
 #pragma unroll
     for (int j8 = 0; j8 < 4; ++j8) {
       const int nn = n + j8 * 8;
@@ -297,19 +309,19 @@ __device__ __forceinline__ void epilogue_act(const GemmParams& p, uint32_t tacc,
       for (int j = 0; j < 8; ++j) u[j] = __uint_as_float(r[j8 * 8 + j]);
       if constexpr (MODE == kFwd) {
         if (bias != nullptr) {
-          load8(bias + nn, a);
+          unpack8(__ldg(reinterpret_cast<const uint4*>(bias + nn)), a);
 #pragma unroll
           for (int j = 0; j < 8; ++j) u[j] += a[j];
         }
         if (p.z != nullptr) store8(z + nn, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = act_value(p.act, u[j]);
-        if constexpr (EPI == kEpiGated) {
+        if constexpr (kFwdGated) {
           float u1[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) u1[j] = __uint_as_float(r1[j8 * 8 + j]);
           if (bias != nullptr) {
-            load8(bias + F + nn, a);
+            unpack8(__ldg(reinterpret_cast<const uint4*>(bias + F + nn)), a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) u1[j] += a[j];
           }
@@ -318,16 +330,16 @@ __device__ __forceinline__ void epilogue_act(const GemmParams& p, uint32_t tacc,
           for (int j = 0; j < 8; ++j) u[j] *= u1[j];
         }
         if (p.residual != nullptr) {
-          load8(res + nn, a);
+          unpack8(g0[j8], a);
 #pragma unroll
           for (int j = 0; j < 8; ++j) u[j] += a[j];
         }
         store8(out + nn, u);
       } else {
-        load8(z + nn, a);
-        if constexpr (EPI == kEpiGated) {
+        unpack8(g0[j8], a);
+        if constexpr (kBwdGated) {
           float z1[8], d1[8];
-          load8(z + F + nn, z1);
+          unpack8(g1[j8], z1);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float value;
@@ -350,9 +362,9 @@ __device__ __forceinline__ void epilogue_act(const GemmParams& p, uint32_t tacc,
 }
 
 template <int MODE, int CG, bool PG, int EPI>
-__global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<MODE, CG, EPI>::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ PGArgs<PG> pg) {
-  using C = Cfg<MODE, CG>;
+  using C = Cfg<MODE, CG, EPI>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
@@ -688,7 +700,7 @@ __global__ void __launch_bounds__(Cfg<MODE, CG>::kThreads, 1)
         const bool row_ok = row >= 0 && row < tl.r1 && row < p.M && row < p.out_rows;
         const __nv_bfloat16* bias = nullptr;
         if (MODE == kFwd && p.has_bias) bias = PG ? pg.b(tl.g) : (p.bias + static_cast<int64_t>(tl.g) * p.N);
-        epilogue_act<MODE, EPI>(p, tacc, row, row_ok, tl.nt * out_tile<MODE, EPI>(), bias, release_acc);
+        epilogue_act<MODE, EPI>(p, tacc, row, row_ok, tl.nt * out_tile<MODE, EPI>(), (warp - 2) >> 2, bias, release_acc);
       } else if (MODE != kWgrad) {
         const int Nout = (MODE == kFwd) ? p.N : p.K;
         const int64_t row = tl.r0 + hr + row_in_tile;
@@ -860,7 +872,7 @@ gl_status launch_one(const GemmParams& prm, const PGArgs<PG>& pga, int G, cudaSt
   const int smem = smem_bytes_for<MODE, CG>(G);
   auto kern = grouped_gemm_kernel<MODE, CG, PG, EPI>;
   if (set_max_smem(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return GL_ERR_CUDA;
-  constexpr int threads = Cfg<MODE, CG>::kThreads;
+  constexpr int threads = Cfg<MODE, CG, EPI>::kThreads;
   const int grid = grid_for(kern, CG, threads, smem);
   if (CG == 1) {
     kern<<<grid, threads, smem, stream>>>(prm, pga);
@@ -874,7 +886,7 @@ gl_status launch_one(const GemmParams& prm, const PGArgs<PG>& pga, int G, cudaSt
 
 template <int MODE, int CG, int EPI = kEpiPlain>
 gl_status launch_mode(const GemmCall& c) {
-  using Cf = Cfg<MODE, CG>;
+  using Cf = Cfg<MODE, CG, EPI>;
   const CUtensorMapDataType BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   GemmParams prm;
   memset(&prm, 0, sizeof(prm));
