@@ -29,42 +29,86 @@ __device__ __forceinline__ float act_sigmoid(float v) { return __fdividef(1.0f, 
 constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// Value of an inner activation.  `act` is the same for the whole launch.
-__device__ __forceinline__ float act_value(int act, float u) {
-  switch (act) {
-    case GL_ACT_RELU: return u < 0.0f ? 0.0f : u;
-    case GL_ACT_RELU2: return u < 0.0f ? 0.0f : u * u;
-    case GL_ACT_GELU: return u * act_sigmoid(kGelu2C * (u + kGeluA * u * u * u));
-    case GL_ACT_SILU: return u * act_sigmoid(u);
-  }
+// One inner activation, known at compile time.
+template <int ACT>
+__device__ __forceinline__ float act_of(float u) {
+  if (ACT == GL_ACT_RELU) return u < 0.0f ? 0.0f : u;
+  if (ACT == GL_ACT_RELU2) return u < 0.0f ? 0.0f : u * u;
+  if (ACT == GL_ACT_GELU) return u * act_sigmoid(u * fmaf(kGelu2C * kGeluA, u * u, kGelu2C));
+  if (ACT == GL_ACT_SILU) return u * act_sigmoid(u);
   return u;
 }
 
-// Value and slope of an inner activation.
-__device__ __forceinline__ float act_slope(int act, float u, float& value) {
-  switch (act) {
-    case GL_ACT_RELU:
-      value = u < 0.0f ? 0.0f : u;
-      return u > 0.0f ? 1.0f : 0.0f;
-    case GL_ACT_RELU2:
-      value = u < 0.0f ? 0.0f : u * u;
-      return u < 0.0f ? 0.0f : 2.0f * u;
-    case GL_ACT_GELU: {
-      const float u2 = u * u;
-      const float q = act_sigmoid(kGelu2C * (u + kGeluA * u2 * u));
-      value = u * q;
-      const float w = q * (1.0f - q);
-      // far out w is 0 and u2 may be infinite: the product's limit is 0
-      return w == 0.0f ? q : fmaf(u * w, kGelu2C * fmaf(3.0f * kGeluA, u2, 1.0f), q);
-    }
-    case GL_ACT_SILU: {
-      const float q = act_sigmoid(u);
-      value = u * q;
-      return q * fmaf(u, 1.0f - q, 1.0f);
-    }
+// Its value and slope.
+template <int ACT>
+__device__ __forceinline__ float slope_of(float u, float& value) {
+  if (ACT == GL_ACT_RELU) {
+    value = u < 0.0f ? 0.0f : u;
+    return u > 0.0f ? 1.0f : 0.0f;
+  }
+  if (ACT == GL_ACT_RELU2) {
+    value = u < 0.0f ? 0.0f : u * u;
+    return u < 0.0f ? 0.0f : 2.0f * u;
+  }
+  if (ACT == GL_ACT_GELU) {
+    const float u2 = u * u;
+    const float q = act_sigmoid(u * fmaf(kGelu2C * kGeluA, u2, kGelu2C));
+    value = u * q;
+    const float w = q * (1.0f - q);
+    // far out w is 0 and u2 may be infinite: the product's limit is 0
+    return w == 0.0f ? q : fmaf(u * w, fmaf(3.0f * kGelu2C * kGeluA, u2, kGelu2C), q);
+  }
+  if (ACT == GL_ACT_SILU) {
+    const float q = act_sigmoid(u);
+    value = u * q;
+    return q * fmaf(u, 1.0f - q, 1.0f);
   }
   value = u;
   return 1.0f;
+}
+
+// f.template operator()<ACT>() for the launch's inner activation: one branch
+// around a loop instead of a chain of them per element.
+template <typename Fn>
+__device__ __forceinline__ void act_dispatch(int act, Fn f) {
+  switch (act) {
+    case GL_ACT_RELU: f.template operator()<GL_ACT_RELU>(); break;
+    case GL_ACT_RELU2: f.template operator()<GL_ACT_RELU2>(); break;
+    case GL_ACT_GELU: f.template operator()<GL_ACT_GELU>(); break;
+    case GL_ACT_SILU: f.template operator()<GL_ACT_SILU>(); break;
+    default: f.template operator()<GL_ACT_NONE>(); break;
+  }
+}
+
+template <int N>
+struct ActValues {
+  float (&u)[N];
+  template <int ACT>
+  __device__ __forceinline__ void operator()() {
+#pragma unroll
+    for (int j = 0; j < N; ++j) u[j] = act_of<ACT>(u[j]);
+  }
+};
+// u[] <- act(u[])
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&u)[N]) {
+  act_dispatch(act, ActValues<N>{u});
+}
+
+template <int N>
+struct ActSlopes {
+  float (&u)[N];
+  float (&value)[N];
+  template <int ACT>
+  __device__ __forceinline__ void operator()() {
+#pragma unroll
+    for (int j = 0; j < N; ++j) u[j] = slope_of<ACT>(u[j], value[j]);
+  }
+};
+// u[] <- act'(u[]), value[] <- act(u[])
+template <int N>
+__device__ __forceinline__ void act_slopes(int act, float (&u)[N], float (&value)[N]) {
+  act_dispatch(act, ActSlopes<N>{u, value});
 }
 
 }  // namespace gl

@@ -64,6 +64,11 @@ constexpr int kSmemBudget = 212992;  // stage ring (pairs: 3 x 64 KB; single CTA
 template <int MODE>
 __host__ __device__ constexpr int band_rows() { return MODE == kFwd ? 16 : 8; }
 
+// The epilogue forms choose by the bytes that a band keeps in L2, its strips
+// of A over the whole contraction: 16 rows while they take up to half of the
+// 126 MB, else 8.
+int band_for(int contraction) { return int64_t(16) * 256 * contraction * 2 <= int64_t(63) << 20 ? 16 : 8; }
+
 // Epilogue forms of FWD and DGRAD.
 enum { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2 };
 
@@ -118,6 +123,7 @@ struct GemmParams {
   int accumulate;
   uint64_t wait_ns;  // bound on each pipeline wait
   int hold_loads;    // testing: the producer issues no loads
+  int band;                       // tile rows per rasterisation band (epilogue forms)
   int act;                        // inner activation of the epilogue forms
   const __nv_bfloat16* residual;  // FWD forms: [M, columns of y] or null
   __nv_bfloat16* z;               // FWD forms: pre-activations [M, N], written, or null; DGRAD forms: read
@@ -185,7 +191,7 @@ __device__ __forceinline__ Tile decode_tile(int t, const int* prefix, const Gemm
   // near-square block and share operand strips through L2.
   const int mtg = (MODE == kWgrad) ? ceil_div_i(p.N, C::kTileM) : ceil_div_i(m, C::kTileM);
   const int ntg = ceil_div_i(out_cols<MODE, EPI>(p), out_tile<MODE, EPI>());
-  constexpr int kBand = band_rows<MODE>();
+  const int kBand = EPI == kEpiPlain ? band_rows<MODE>() : p.band;
   const int band = local / (kBand * ntg);
   const int base_mt = band * kBand;
   const int bh = min(kBand, mtg - base_mt);
@@ -245,7 +251,7 @@ __device__ __forceinline__ void zero_tail_rows(uint8_t* sa, uint8_t* sb, int r_f
 }
 
 // Eight bf16 values as fp32.
-__device__ __forceinline__ void unpack8(const uint4& w, float* v) {
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
   const __nv_bfloat16* b = reinterpret_cast<const __nv_bfloat16*>(&w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = __bfloat162float(b[j]);
@@ -257,7 +263,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
   w.y = pack_bf16x2(v[2], v[3]);
   w.z = pack_bf16x2(v[4], v[5]);
   w.w = pack_bf16x2(v[6], v[7]);
-  *reinterpret_cast<uint4*>(p) = w;
+  __stcs(reinterpret_cast<uint4*>(p), w);
 }
 
 // 32 accumulator columns of this thread's TMEM lane.
@@ -288,12 +294,18 @@ __device__ __forceinline__ void epilogue_act(const GemmParams& p, uint32_t tacc,
   if (half >= nchunks) release();  // this warp's chunks lie past the last column
   for (int c = half; c < nchunks; c += 2) {
     const int n = n0 + c * 32;
-    uint4 g0[4], g1[kBwdGated ? 4 : 1];
+    uint4 g0[4], g1[kBwdGated ? 4 : 1], b0[MODE == kFwd ? 4 : 1], b1[kFwdGated ? 4 : 1];
 #pragma unroll
     for (int j8 = 0; j8 < 4; ++j8) {
       if (reads && n + j8 * 8 < F) {
-        g0[j8] = *reinterpret_cast<const uint4*>(src + n + j8 * 8);
-        if constexpr (kBwdGated) g1[j8] = *reinterpret_cast<const uint4*>(src + F + n + j8 * 8);
+        g0[j8] = __ldcs(reinterpret_cast<const uint4*>(src + n + j8 * 8));
+        if constexpr (kBwdGated) g1[j8] = __ldcs(reinterpret_cast<const uint4*>(src + F + n + j8 * 8));
+      }
+      if constexpr (MODE == kFwd) {
+        if (bias != nullptr && n + j8 * 8 < F) {
+          b0[j8] = __ldg(reinterpret_cast<const uint4*>(bias + n + j8 * 8));
+          if constexpr (kFwdGated) b1[j8] = __ldg(reinterpret_cast<const uint4*>(bias + F + n + j8 * 8));
+        }
       }
     }
     uint32_t r[32], r1[kFwdGated ? 32 : 1];
@@ -309,19 +321,18 @@ __device__ __forceinline__ void epilogue_act(const GemmParams& p, uint32_t tacc,
       for (int j = 0; j < 8; ++j) u[j] = __uint_as_float(r[j8 * 8 + j]);
       if constexpr (MODE == kFwd) {
         if (bias != nullptr) {
-          unpack8(__ldg(reinterpret_cast<const uint4*>(bias + nn)), a);
+          unpack8(b0[j8], a);
 #pragma unroll
           for (int j = 0; j < 8; ++j) u[j] += a[j];
         }
         if (p.z != nullptr) store8(z + nn, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = act_value(p.act, u[j]);
+        act_values(p.act, u);
         if constexpr (kFwdGated) {
           float u1[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) u1[j] = __uint_as_float(r1[j8 * 8 + j]);
           if (bias != nullptr) {
-            unpack8(__ldg(reinterpret_cast<const uint4*>(bias + F + nn)), a);
+            unpack8(b1[j8], a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) u1[j] += a[j];
           }
@@ -336,24 +347,20 @@ __device__ __forceinline__ void epilogue_act(const GemmParams& p, uint32_t tacc,
         }
         store8(out + nn, u);
       } else {
+        float value[8];
         unpack8(g0[j8], a);
+        act_slopes(p.act, a, value);
         if constexpr (kBwdGated) {
-          float z1[8], d1[8];
+          float z1[8];
           unpack8(g1[j8], z1);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float value;
-            const float slope = act_slope(p.act, a[j], value);
-            d1[j] = u[j] * value;
-            u[j] *= z1[j] * slope;
-          }
-          store8(out + F + nn, d1);
+          for (int j = 0; j < 8; ++j) value[j] *= u[j];
+          store8(out + F + nn, value);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] *= z1[j] * a[j];
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float value;
-            u[j] *= act_slope(p.act, a[j], value);
-          }
+          for (int j = 0; j < 8; ++j) u[j] *= a[j];
         }
         store8(out + nn, u);
       }
@@ -901,6 +908,7 @@ gl_status launch_mode(const GemmCall& c) {
   prm.hold_loads = c.hold_loads;
   prm.has_bias = (MODE == kFwd && c.bias != nullptr) ? 1 : 0;
   prm.act = act_inner(c.act);
+  prm.band = band_for(MODE == kFwd ? c.K : c.N);
   prm.residual = static_cast<const __nv_bfloat16*>(c.residual);
   prm.z = static_cast<__nv_bfloat16*>(c.z);
   // a gated forward loads W in boxes of 128 rows, whatever the tile shape

@@ -815,8 +815,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int et = tid - 128;           // 0..127
     int it = 0;
     auto store_h = [&](int slot, int f, float u0, float u1) {
-      if (f < p.F)
-        p.hbuf[static_cast<int64_t>(slot) * p.F + f] = __float2bfloat16_rn(act_value(p.act, u0) * u1);
+      float a[1] = {u0};
+      act_values(p.act, a);
+      if (f < p.F) p.hbuf[static_cast<int64_t>(slot) * p.F + f] = __float2bfloat16_rn(a[0] * u1);
     };
     const bool ok = for_segments(f1, cta, [&](const Segment& s) {
       const int buf = it & 1;
