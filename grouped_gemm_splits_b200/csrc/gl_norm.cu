@@ -13,12 +13,20 @@
 // One row is held in registers by one block (or by one warp when it is short),
 // so every input is read once.  A thread owns the 8-column vectors tid,
 // tid + threads, ...: four neighbouring lanes hold one 32-column MXFP8 block.
-// Bound by HBM: 6-8 bytes per element move and some 20 instructions run.
+//
+// Bound by HBM: 6-8 bytes per element move.  Each thread copies its own
+// vectors of the rows to come into its own places of a shared-memory ring
+// (cp.async, kDepth rows ahead) and reads them back itself, so some 190 KB per
+// SM are in flight whatever the block is doing and the ring needs no barrier;
+// without it, with the loads at the head of each row, 65536 x 7168 to MXFP8
+// ran 810 us (47% of HBM, warps waiting for loads).  The arithmetic is done
+// on pairs of columns (f32x2 instructions), gamma stays in registers.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
 #include "gl_internal.h"
+#include "gl_ptx.cuh"
 
 namespace gl {
 namespace {
@@ -26,30 +34,60 @@ namespace {
 constexpr int kMaxThreads = 1024;  // two vectors a thread: GL_NORM_MAX_COLS = 16384 columns
 static_assert(GL_NORM_MAX_COLS == kMaxThreads * 16, "a row fits one block");
 constexpr int kWarpRowThreads = 256;  // eight rows per block when a warp takes a row
+constexpr int kDepth = 3;             // rows in flight, forward (x and residual)
+constexpr int kBwdDepth = 2;          // backward (dy, sum and dsum)
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+// ------------------------------------------------------- pairs of fp32 values
+typedef uint64_t f2;
+__device__ __forceinline__ f2 f2_make(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_get(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// two bf16 values
+__device__ __forceinline__ f2 f2_of_bf16(uint32_t w) {
+  return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t bf16_of_f2(f2 v) {
+  const float2 t = f2_get(v);
+  __nv_bfloat162 h = __floats2bfloat162_rn(t.x, t.y);
+  return *reinterpret_cast<uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    u[i] = *reinterpret_cast<uint32_t*>(&h);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
+// One vector: eight bf16 values, or four pairs.
+struct Words {
+  uint32_t w[4];
+};
+__device__ __forceinline__ Words words(const uint4& v) { return Words{{v.x, v.y, v.z, v.w}}; }
+__device__ __forceinline__ uint4 pack_vec(const f2 (&v)[4]) {
+  return make_uint4(bf16_of_f2(v[0]), bf16_of_f2(v[1]), bf16_of_f2(v[2]), bf16_of_f2(v[3]));
 }
 
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t e4m3x4(f2 a, f2 b) {
+  const float2 u = f2_get(a), v = f2_get(b);
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(u.y), "f"(u.x));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v.y), "f"(v.x));
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
@@ -59,6 +97,20 @@ __device__ __forceinline__ int e8m0_of(float amax) {
   if (amax == 0.0f) return 127;
   const uint32_t b = __float_as_uint(amax);
   return max(0, static_cast<int>((b + 0x1FFFFFu) >> 23) - 8);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -94,74 +146,121 @@ struct NormParams {
   int mma_scales;
 };
 
-// x, residual and the outputs may be the same buffers: a thread reads all of
-// its row's vectors before it writes any, and no other thread touches them.
+// The ring: kTensors tensors x kDepth rows, one 16-byte place per thread and
+// vector.  A thread refills a place only after it has used what it read there.
+template <int VPT, int TENSORS, int DEPTH>
+struct Ring {
+  uint32_t base;  // this thread's first place
+  uint32_t pitch;  // bytes from one vector of the block to the next
+  __device__ __forceinline__ uint32_t place(int slot, int tensor, int j) const {
+    return base + ((slot * TENSORS + tensor) * VPT + j) * pitch;
+  }
+  static constexpr int bytes(int threads) { return DEPTH * TENSORS * VPT * threads * 16; }
+};
+
+// x, residual and the outputs may be the same buffers: a thread has read all
+// of its row's vectors before it writes any, and no other thread touches them.
 template <int VPT, bool WARP_ROW, bool MX>
 __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     rmsnorm_kernel(const NormParams p) {
+  extern __shared__ __align__(16) uint8_t ring_s[];
   __shared__ float part[2][32];
   const int tpr = WARP_ROW ? 32 : static_cast<int>(blockDim.x);
   const int t = WARP_ROW ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int rpb = WARP_ROW ? kWarpRowThreads / 32 : 1;
   const int nv = p.cols >> 3;
-  int buf = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rpb + (WARP_ROW ? (threadIdx.x >> 5) : 0); row < p.rows;
-       row += static_cast<int64_t>(gridDim.x) * rpb, buf ^= 1) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * rpb;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpb + (WARP_ROW ? (threadIdx.x >> 5) : 0);
+  const Ring<VPT, 2, kDepth> ring{smem_u32(ring_s) + threadIdx.x * 16, blockDim.x * 16};
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
+  const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(p.residual);
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int c = t + j * tpr;
+        if (c < nv) {
+          const int64_t at = row * p.cols + c * 8;
+          cp_async16(ring.place(slot, 0, j), x + at);
+          if (res != nullptr) cp_async16(ring.place(slot, 1, j), res + at);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) fetch(row0 + i * stride, i);
+  Words g[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = t + j * tpr;
+    g[j] = words(c < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma) + c) : make_uint4(0, 0, 0, 0));
+  }
+  const float inv_n = 1.0f / static_cast<float>(p.cols);
+  const int64_t atoms = (p.rows + 127) >> 7;  // MMA layout: atoms per k-group
+  int slot = 0, buf = 0;
+  for (int64_t row = row0; row < p.rows; row += stride, buf ^= 1) {
     const int64_t base = row * p.cols;
-    float v[VPT][8];
-    float ss = 0.0f;
+    f2 v[VPT][4];
+    f2 ss = 0;
+    cp_async_wait<kDepth - 1>();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int c = t + j * tpr;
-      if (c < nv) {
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + base + c * 8), v[j]);
-        if (p.residual != nullptr) {
-          float r[8];
-          unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + base + c * 8), r);
+      if (t + j * tpr < nv) {
+        const Words a = words(lds16(ring.place(slot, 0, j)));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[j][i] += r[i];
+        for (int i = 0; i < 4; ++i) v[j][i] = f2_of_bf16(a.w[i]);
+        if (res != nullptr) {
+          const Words r = words(lds16(ring.place(slot, 1, j)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[j][i] = f2_add(v[j][i], f2_of_bf16(r.w[i]));
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) v[j][i] = 0;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+      for (int i = 0; i < 4; ++i) ss = f2_fma(v[j][i], v[j][i], ss);
     }
-    ss = row_sum<WARP_ROW>(ss, part[buf]);
-    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
+    const float2 s2 = f2_get(ss);
+    const float sum = row_sum<WARP_ROW>(s2.x + s2.y, part[buf]);
+    fetch(row + kDepth * stride, slot);
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
+    const float rstd = 1.0f / sqrtf(fmaf(sum, inv_n, p.eps));
     if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+    const f2 rr = f2_make(rstd, rstd);
+    const int64_t srow = !MX ? 0 : p.mma_scales ? (row >> 7) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4
+                                                : row * (p.cols >> 5);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = t + j * tpr;
       const bool in = c < nv;
       if (in && p.sum != nullptr)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + base + c * 8) = pack8(v[j]);
-      float g[8] = {};
-      if (in) unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.gamma) + c * 8)), g);
+        __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + base + c * 8), pack_vec(v[j]));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * rstd * g[i];
+      for (int i = 0; i < 4; ++i) v[j][i] = f2_mul(f2_mul(v[j][i], rr), f2_of_bf16(g[j].w[i]));
       if (in && p.y != nullptr)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + base + c * 8) = pack8(v[j]);
+        __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + base + c * 8), pack_vec(v[j]));
       if (MX) {
         float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[j][i]));
+        for (int i = 0; i < 4; ++i) {
+          const float2 u = f2_get(v[j][i]);
+          amax = fmaxf(amax, fmaxf(fabsf(u.x), fabsf(u.y)));
+        }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const int e = e8m0_of(amax);
         const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^-(e - 127)
+        const f2 ii = f2_make(inv, inv);
         if (in) {
-          uint2 q;
-          q.x = e4m3x4(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv);
-          q.y = e4m3x4(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv);
-          *reinterpret_cast<uint2*>(p.codes + base + c * 8) = q;
+          const uint2 q = make_uint2(e4m3x4(f2_mul(v[j][0], ii), f2_mul(v[j][1], ii)),
+                                     e4m3x4(f2_mul(v[j][2], ii), f2_mul(v[j][3], ii)));
+          __stcs(reinterpret_cast<uint2*>(p.codes + base + c * 8), q);
           if ((c & 3) == 0) {
             const int kb = c >> 2;
-            const int64_t at = p.mma_scales ? (static_cast<int64_t>(kb >> 2) * ((p.rows + 127) >> 7) + (row >> 7)) * 512 +
-                                                  (row & 31) * 16 + ((row & 127) >> 5) * 4 + (kb & 3)
-                                            : row * (p.cols >> 5) + kb;
-            p.scales[at] = static_cast<uint8_t>(e);
+            p.scales[srow + (p.mma_scales ? static_cast<int64_t>(kb >> 2) * atoms * 512 + (kb & 3) : kb)] =
+                static_cast<uint8_t>(e);
           }
         }
       }
@@ -184,62 +283,91 @@ struct NormBwdParams {
 template <int VPT, bool WARP_ROW>
 __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     rmsnorm_bwd_kernel(const NormBwdParams p) {
+  extern __shared__ __align__(16) uint8_t ring_s[];
   __shared__ float part[2][32];
-  __shared__ float acc_s[WARP_ROW ? VPT * 256 : 1];
+  __shared__ __align__(16) float acc_s[WARP_ROW ? VPT * 256 : 4];
   const int tpr = WARP_ROW ? 32 : static_cast<int>(blockDim.x);
   const int t = WARP_ROW ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int rpb = WARP_ROW ? kWarpRowThreads / 32 : 1;
   const int nv = p.cols >> 3;
-  float acc[VPT][8] = {};
-  int buf = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rpb + (WARP_ROW ? (threadIdx.x >> 5) : 0); row < p.rows;
-       row += static_cast<int64_t>(gridDim.x) * rpb, buf ^= 1) {
-    const int64_t base = row * p.cols;
-    const float rstd = p.rstd[row];
-    uint4 dyw[VPT], sw[VPT];
-    float dot = 0.0f;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * rpb;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpb + (WARP_ROW ? (threadIdx.x >> 5) : 0);
+  const Ring<VPT, 3, kBwdDepth> ring{smem_u32(ring_s) + threadIdx.x * 16, blockDim.x * 16};
+  const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(p.dy);
+  const __nv_bfloat16* sum = static_cast<const __nv_bfloat16*>(p.sum);
+  const __nv_bfloat16* dsum = static_cast<const __nv_bfloat16*>(p.dsum);
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < p.rows) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = t + j * tpr;
-      dyw[j] = sw[j] = make_uint4(0, 0, 0, 0);
-      if (c < nv) {
-        dyw[j] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dy) + base + c * 8);
-        sw[j] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.sum) + base + c * 8);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = t + j * tpr;
-      if (c < nv) {
-        float d[8], s[8], g[8];
-        unpack8(dyw[j], d);
-        unpack8(sw[j], s);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.gamma) + c * 8)), g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float dh = d[i] * (s[i] * rstd);
-          acc[j][i] += dh;
-          dot = fmaf(dh, g[i], dot);
+      for (int j = 0; j < VPT; ++j) {
+        const int c = t + j * tpr;
+        if (c < nv) {
+          const int64_t at = row * p.cols + c * 8;
+          cp_async16(ring.place(slot, 0, j), dy + at);
+          cp_async16(ring.place(slot, 1, j), sum + at);
+          if (dsum != nullptr) cp_async16(ring.place(slot, 2, j), dsum + at);
         }
       }
     }
-    dot = row_sum<WARP_ROW>(dot, part[buf]) / static_cast<float>(p.cols);
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kBwdDepth; ++i) fetch(row0 + i * stride, i);
+  Words g[VPT];
+  f2 acc[VPT][4];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = t + j * tpr;
+    g[j] = words(c < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma) + c) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0;
+  }
+  const float inv_n = 1.0f / static_cast<float>(p.cols);
+  float next_rstd = row0 < p.rows ? __ldg(p.rstd + row0) : 0.0f;
+  int slot = 0, buf = 0;
+  for (int64_t row = row0; row < p.rows; row += stride, buf ^= 1) {
+    const int64_t base = row * p.cols;
+    const float rstd = next_rstd;
+    if (row + stride < p.rows) next_rstd = __ldg(p.rstd + row + stride);
+    const f2 rr = f2_make(rstd, rstd);
+    f2 dot2 = 0;
+    cp_async_wait<kBwdDepth - 1>();
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (t + j * tpr < nv) {
+        const Words d = words(lds16(ring.place(slot, 0, j))), x = words(lds16(ring.place(slot, 1, j)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 dh = f2_mul(f2_of_bf16(d.w[i]), f2_mul(f2_of_bf16(x.w[i]), rr));
+          acc[j][i] = f2_add(acc[j][i], dh);
+          dot2 = f2_fma(dh, f2_of_bf16(g[j].w[i]), dot2);
+        }
+      }
+    }
+    const float2 d2 = f2_get(dot2);
+    const float dot = row_sum<WARP_ROW>(d2.x + d2.y, part[buf]) * inv_n;
+    // dx = rstd * (dy gamma - s rstd dot) + dsum; the row is read a second time
+    // from the ring (keeping it in registers would halve the threads per SM)
+    const f2 md = f2_make(-dot * rstd, -dot * rstd);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = t + j * tpr;
       if (c < nv) {
-        float d[8], s[8], g[8], r[8] = {};
-        unpack8(dyw[j], d);
-        unpack8(sw[j], s);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.gamma) + c * 8)), g);
-        if (p.dsum != nullptr)
-          unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dsum) + base + c * 8), r);
+        const Words d = words(lds16(ring.place(slot, 0, j))), x = words(lds16(ring.place(slot, 1, j)));
+        const Words e = words(dsum != nullptr ? lds16(ring.place(slot, 2, j)) : make_uint4(0, 0, 0, 0));
+        f2 o[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = rstd * (d[i] * g[i] - (s[i] * rstd) * dot) + r[i];
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dx) + base + c * 8) = pack8(d);
+        for (int i = 0; i < 4; ++i) {
+          const f2 gd = f2_mul(f2_of_bf16(d.w[i]), f2_of_bf16(g[j].w[i]));
+          o[i] = f2_fma(f2_fma(f2_of_bf16(x.w[i]), md, gd), rr, f2_of_bf16(e.w[i]));
+        }
+        __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dx) + base + c * 8), pack_vec(o));
       }
     }
+    fetch(row + kBwdDepth * stride, slot);
+    slot = slot + 1 == kBwdDepth ? 0 : slot + 1;
   }
+  grid_launch_dependents();
   float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.cols;
   if (WARP_ROW) {  // the block's eight warps hold the same columns: add them in warp order
     for (int w = 0; w < kWarpRowThreads / 32; ++w) {
@@ -247,9 +375,9 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int at = (t + j * 32) * 8 + i;
-            acc_s[at] = (w == 0 ? 0.0f : acc_s[at]) + acc[j][i];
+          for (int i = 0; i < 4; ++i) {
+            f2* at = reinterpret_cast<f2*>(acc_s) + (t + j * 32) * 4 + i;
+            *at = w == 0 ? acc[j][i] : f2_add(*at, acc[j][i]);
           }
       }
       __syncthreads();
@@ -260,32 +388,43 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     for (int j = 0; j < VPT; ++j) {
       const int c = t + j * tpr;
       if (c < nv) {
-        *reinterpret_cast<float4*>(out + c * 8) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-        *reinterpret_cast<float4*>(out + c * 8 + 4) = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+        *reinterpret_cast<ulonglong2*>(out + c * 8) = make_ulonglong2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<ulonglong2*>(out + c * 8 + 4) = make_ulonglong2(acc[j][2], acc[j][3]);
       }
     }
   }
 }
 
-// dgamma[c] (+)= the blocks' partial sums, in a fixed order: eight warps take
-// the blocks w, w + 8, ... of 32 columns, then the eight sums are added.
-__global__ void __launch_bounds__(256)
+// dgamma[c] (+)= the blocks' partial sums, in a fixed order: 32 warps take the
+// blocks w, w + 32, ... of 32 columns, four at a time, then the 32 sums are
+// added.
+constexpr int kDgThreads = 1024;
+__global__ void __launch_bounds__(kDgThreads)
     rmsnorm_dgamma_kernel(const float* __restrict__ part, int blocks, int cols, float* __restrict__ dgamma,
                           int accumulate) {
-  __shared__ float sm[8][32];
+  __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  const float old = (w == 0 && c < cols && accumulate) ? dgamma[c] : 0.0f;
   float s = 0.0f;
-  if (c < cols)
-    for (int b = w; b < blocks; b += 8) s += part[static_cast<int64_t>(b) * cols + c];
+  grid_dependency_wait();
+  if (c < cols) {
+    int b = w;
+    for (; b + 96 < blocks; b += 128) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = part[static_cast<int64_t>(b + 32 * i) * cols + c];
+      s += (v[0] + v[1]) + (v[2] + v[3]);
+    }
+    for (; b < blocks; b += 32) s += part[static_cast<int64_t>(b) * cols + c];
+  }
   sm[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < cols) {
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += sm[i][lane];
-    dgamma[c] = accumulate ? dgamma[c] + s : s;
-  }
+  s = warp_sum(sm[lane][w]);  // warp w: the sums of column w
+  __syncthreads();
+  if (lane == 0) sm[0][w] = s;
+  __syncthreads();
+  if (w == 0 && c < cols) dgamma[c] = old + sm[0][lane];
 }
 
 struct NormPlan {
@@ -311,25 +450,38 @@ NormPlan plan_for(int cols) {
   return pl;
 }
 
-int blocks_for(const NormPlan& pl, int64_t rows, int threads_per_sm) {
+// One wave: the rings of the blocks of an SM (2048 vectors' places, 192 KB)
+// fill its shared memory.
+int blocks_for(const NormPlan& pl, int64_t rows) {
   const int64_t need = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
-  const int64_t fit = static_cast<int64_t>(num_sms()) * std::max(1, threads_per_sm / pl.threads);
+  const int64_t fit = static_cast<int64_t>(num_sms()) * std::max(1, 2048 / (pl.threads * pl.vpt));
   return static_cast<int>(std::min(need, fit));
 }
 
-template <bool MX>
-void launch_fwd(const NormPlan& pl, int grid, const NormParams& p, cudaStream_t s) {
-  if (pl.warp_row) {
-    if (pl.vpt == 1) rmsnorm_kernel<1, true, MX><<<grid, pl.threads, 0, s>>>(p);
-    else if (pl.vpt == 2) rmsnorm_kernel<2, true, MX><<<grid, pl.threads, 0, s>>>(p);
-    else rmsnorm_kernel<4, true, MX><<<grid, pl.threads, 0, s>>>(p);
-  } else {
-    rmsnorm_kernel<2, false, MX><<<grid, pl.threads, 0, s>>>(p);
-  }
+template <int VPT, bool WARP_ROW, bool MX>
+gl_status run_fwd(const NormPlan& pl, int grid, const NormParams& p, cudaStream_t s) {
+  auto kern = rmsnorm_kernel<VPT, WARP_ROW, MX>;
+  const int smem = Ring<VPT, 2, kDepth>::bytes(pl.threads);
+  if (set_max_smem(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return GL_ERR_CUDA;
+  kern<<<grid, pl.threads, smem, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GL_OK : GL_ERR_CUDA;
 }
 
-constexpr int kFwdThreadsPerSm = 2048;
-constexpr int kBwdThreadsPerSm = 1024;
+template <bool MX>
+gl_status launch_fwd(const NormPlan& pl, int grid, const NormParams& p, cudaStream_t s) {
+  if (!pl.warp_row) return run_fwd<2, false, MX>(pl, grid, p, s);
+  if (pl.vpt == 1) return run_fwd<1, true, MX>(pl, grid, p, s);
+  return pl.vpt == 2 ? run_fwd<2, true, MX>(pl, grid, p, s) : run_fwd<4, true, MX>(pl, grid, p, s);
+}
+
+template <int VPT, bool WARP_ROW>
+gl_status run_bwd(const NormPlan& pl, int grid, const NormBwdParams& p, cudaStream_t s) {
+  auto kern = rmsnorm_bwd_kernel<VPT, WARP_ROW>;
+  const int smem = Ring<VPT, 3, kBwdDepth>::bytes(pl.threads);
+  if (set_max_smem(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return GL_ERR_CUDA;
+  kern<<<grid, pl.threads, smem, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GL_OK : GL_ERR_CUDA;
+}
 
 }  // namespace
 
@@ -338,13 +490,11 @@ gl_status launch_rmsnorm(const void* x, const void* residual, const void* gamma,
                          cudaStream_t stream) {
   const NormPlan pl = plan_for(cols);
   NormParams p{x, residual, gamma, eps, rows, cols, sum, y, rstd, codes, scales, scale_layout == GL_SCALES_MMA};
-  const int grid = blocks_for(pl, rows, kFwdThreadsPerSm);
-  if (codes != nullptr) launch_fwd<true>(pl, grid, p, stream);
-  else launch_fwd<false>(pl, grid, p, stream);
-  return cudaGetLastError() == cudaSuccess ? GL_OK : GL_ERR_CUDA;
+  const int grid = blocks_for(pl, rows);
+  return codes != nullptr ? launch_fwd<true>(pl, grid, p, stream) : launch_fwd<false>(pl, grid, p, stream);
 }
 
-int64_t rmsnorm_bwd_blocks(int64_t rows, int cols) { return blocks_for(plan_for(cols), rows, kBwdThreadsPerSm); }
+int64_t rmsnorm_bwd_blocks(int64_t rows, int cols) { return blocks_for(plan_for(cols), rows); }
 
 gl_status launch_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma, const float* rstd, const void* dsum,
                              int64_t rows, int cols, void* dx, float* dgamma, int accumulate, float* part,
@@ -353,17 +503,25 @@ gl_status launch_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma,
   const int grid = static_cast<int>(rmsnorm_bwd_blocks(rows, cols));
   NormBwdParams p{dy, sum, gamma, rstd, dsum, rows, cols, dx, part};
   if (grid > 0) {
-    if (pl.warp_row) {
-      if (pl.vpt == 1) rmsnorm_bwd_kernel<1, true><<<grid, pl.threads, 0, stream>>>(p);
-      else if (pl.vpt == 2) rmsnorm_bwd_kernel<2, true><<<grid, pl.threads, 0, stream>>>(p);
-      else rmsnorm_bwd_kernel<4, true><<<grid, pl.threads, 0, stream>>>(p);
-    } else {
-      rmsnorm_bwd_kernel<2, false><<<grid, pl.threads, 0, stream>>>(p);
-    }
-    if (cudaGetLastError() != cudaSuccess) return GL_ERR_CUDA;
+    const gl_status st = !pl.warp_row     ? run_bwd<2, false>(pl, grid, p, stream)
+                         : pl.vpt == 1 ? run_bwd<1, true>(pl, grid, p, stream)
+                         : pl.vpt == 2 ? run_bwd<2, true>(pl, grid, p, stream)
+                                       : run_bwd<4, true>(pl, grid, p, stream);
+    if (st != GL_OK) return st;
   }
-  rmsnorm_dgamma_kernel<<<(cols + 31) / 32, 256, 0, stream>>>(part, grid, cols, dgamma, accumulate);
-  return cudaGetLastError() == cudaSuccess ? GL_OK : GL_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((cols + 31) / 32);
+  cfg.blockDim = dim3(kDgThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];  // its blocks may start while the last of the rows are worked on
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = grid > 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rmsnorm_dgamma_kernel, static_cast<const float*>(part), grid, cols, dgamma,
+                            accumulate) == cudaSuccess
+             ? GL_OK
+             : GL_ERR_CUDA;
 }
 
 }  // namespace gl
