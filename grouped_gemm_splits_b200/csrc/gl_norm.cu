@@ -16,11 +16,19 @@
 //
 // Bound by HBM: 6-8 bytes per element move.  Each thread copies its own
 // vectors of the rows to come into its own places of a shared-memory ring
-// (cp.async, kDepth rows ahead) and reads them back itself, so some 190 KB per
-// SM are in flight whatever the block is doing and the ring needs no barrier;
-// without it, with the loads at the head of each row, 65536 x 7168 to MXFP8
-// ran 810 us (47% of HBM, warps waiting for loads).  The arithmetic is done
-// on pairs of columns (f32x2 instructions), gamma stays in registers.
+// (cp.async) and reads them back itself, so loads are in flight whatever the
+// block is doing and the ring needs no barrier; with the loads at the head of
+// each row instead, 65536 x 7168 to MXFP8 ran 810 us (47% of HBM, warps waiting
+// for loads).  The arithmetic is done on pairs of columns (f32x2
+// instructions), gamma stays in registers.
+//
+// How much is in flight: enough threads for the arithmetic (768-1024 per SM)
+// and no more rows than that takes.  More blocks or a deeper ring make reads
+// and writes meet in DRAM: 32768 x 4096 to MXFP8 took 147 us with two blocks of
+// 512 and two rows each in flight, 155 us with three rows, 179 us with four
+// blocks of 256 (two vectors a thread) and three rows; the floor is 144 us.
+// Measured with it: 65536 x 7168 to MXFP8 511 us (floor 504), to bf16 571
+// (574); 32768 x 2048 81 (72) and 88 (82); backward 32768 x 4096 164 (164).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -34,8 +42,7 @@ namespace {
 constexpr int kMaxThreads = 1024;  // two vectors a thread: GL_NORM_MAX_COLS = 16384 columns
 static_assert(GL_NORM_MAX_COLS == kMaxThreads * 16, "a row fits one block");
 constexpr int kWarpRowThreads = 256;  // eight rows per block when a warp takes a row
-constexpr int kDepth = 3;             // rows in flight, forward (x and residual)
-constexpr int kBwdDepth = 2;          // backward (dy, sum and dsum)
+constexpr int kWarpRowCols = 256;     // up to here: one vector a lane
 
 // ------------------------------------------------------- pairs of fp32 values
 typedef uint64_t f2;
@@ -146,7 +153,7 @@ struct NormParams {
   int mma_scales;
 };
 
-// The ring: kTensors tensors x kDepth rows, one 16-byte place per thread and
+// The ring: TENSORS tensors x DEPTH rows, one 16-byte place per thread and
 // vector.  A thread refills a place only after it has used what it read there.
 template <int VPT, int TENSORS, int DEPTH>
 struct Ring {
@@ -160,7 +167,7 @@ struct Ring {
 
 // x, residual and the outputs may be the same buffers: a thread has read all
 // of its row's vectors before it writes any, and no other thread touches them.
-template <int VPT, bool WARP_ROW, bool MX>
+template <int VPT, bool WARP_ROW, bool MX, int DEPTH>
 __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     rmsnorm_kernel(const NormParams p) {
   extern __shared__ __align__(16) uint8_t ring_s[];
@@ -171,7 +178,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
   const int nv = p.cols >> 3;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * rpb;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpb + (WARP_ROW ? (threadIdx.x >> 5) : 0);
-  const Ring<VPT, 2, kDepth> ring{smem_u32(ring_s) + threadIdx.x * 16, blockDim.x * 16};
+  const Ring<VPT, 2, DEPTH> ring{smem_u32(ring_s) + threadIdx.x * 16, blockDim.x * 16};
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
   const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(p.residual);
   auto fetch = [&](int64_t row, int slot) {
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kDepth; ++i) fetch(row0 + i * stride, i);
+  for (int i = 0; i < DEPTH; ++i) fetch(row0 + i * stride, i);
   Words g[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     const int64_t base = row * p.cols;
     f2 v[VPT][4];
     f2 ss = 0;
-    cp_async_wait<kDepth - 1>();
+    cp_async_wait<DEPTH - 1>();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (t + j * tpr < nv) {
@@ -224,8 +231,8 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     }
     const float2 s2 = f2_get(ss);
     const float sum = row_sum<WARP_ROW>(s2.x + s2.y, part[buf]);
-    fetch(row + kDepth * stride, slot);
-    slot = slot + 1 == kDepth ? 0 : slot + 1;
+    fetch(row + DEPTH * stride, slot);
+    slot = slot + 1 == DEPTH ? 0 : slot + 1;
     const float rstd = 1.0f / sqrtf(fmaf(sum, inv_n, p.eps));
     if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
     const f2 rr = f2_make(rstd, rstd);
@@ -280,7 +287,7 @@ struct NormBwdParams {
   float* part;  // [grid, cols] sums of dy * xh over a block's rows
 };
 
-template <int VPT, bool WARP_ROW>
+template <int VPT, bool WARP_ROW, int DEPTH>
 __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     rmsnorm_bwd_kernel(const NormBwdParams p) {
   extern __shared__ __align__(16) uint8_t ring_s[];
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
   const int nv = p.cols >> 3;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * rpb;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpb + (WARP_ROW ? (threadIdx.x >> 5) : 0);
-  const Ring<VPT, 3, kBwdDepth> ring{smem_u32(ring_s) + threadIdx.x * 16, blockDim.x * 16};
+  const Ring<VPT, 3, DEPTH> ring{smem_u32(ring_s) + threadIdx.x * 16, blockDim.x * 16};
   const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(p.dy);
   const __nv_bfloat16* sum = static_cast<const __nv_bfloat16*>(p.sum);
   const __nv_bfloat16* dsum = static_cast<const __nv_bfloat16*>(p.dsum);
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kBwdDepth; ++i) fetch(row0 + i * stride, i);
+  for (int i = 0; i < DEPTH; ++i) fetch(row0 + i * stride, i);
   Words g[VPT];
   f2 acc[VPT][4];
 #pragma unroll
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     if (row + stride < p.rows) next_rstd = __ldg(p.rstd + row + stride);
     const f2 rr = f2_make(rstd, rstd);
     f2 dot2 = 0;
-    cp_async_wait<kBwdDepth - 1>();
+    cp_async_wait<DEPTH - 1>();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (t + j * tpr < nv) {
@@ -364,8 +371,8 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
         __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dx) + base + c * 8), pack_vec(o));
       }
     }
-    fetch(row + kBwdDepth * stride, slot);
-    slot = slot + 1 == kBwdDepth ? 0 : slot + 1;
+    fetch(row + DEPTH * stride, slot);
+    slot = slot + 1 == DEPTH ? 0 : slot + 1;
   }
   grid_launch_dependents();
   float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.cols;
@@ -432,52 +439,51 @@ struct NormPlan {
   int vpt, threads, rows_per_block;
 };
 
-// Rows of up to 1024 columns go to one warp each.  Longer rows take a block of
-// two vectors a thread.
+// Short rows go to one warp each, up to 8192 columns to a block of one vector
+// a thread (two or four vectors were slower at every width: fewer threads per
+// row in flight), wider ones to a block of two.
 NormPlan plan_for(int cols) {
   const int nv = cols >> 3;
   NormPlan pl;
-  pl.warp_row = nv <= 128;
-  if (pl.warp_row) {
-    pl.vpt = nv <= 32 ? 1 : nv <= 64 ? 2 : 4;
-    pl.threads = kWarpRowThreads;
-    pl.rows_per_block = kWarpRowThreads / 32;
-  } else {
-    pl.vpt = 2;
-    pl.threads = ((nv + pl.vpt - 1) / pl.vpt + 31) / 32 * 32;
-    pl.rows_per_block = 1;
-  }
+  pl.warp_row = cols <= kWarpRowCols;
+  pl.vpt = nv <= kMaxThreads ? 1 : 2;
+  pl.threads = pl.warp_row ? kWarpRowThreads : ((nv + pl.vpt - 1) / pl.vpt + 31) / 32 * 32;
+  pl.rows_per_block = pl.warp_row ? kWarpRowThreads / 32 : 1;
   return pl;
 }
 
-// One wave: the rings of the blocks of an SM (2048 vectors' places, 192 KB)
-// fill its shared memory.
-int blocks_for(const NormPlan& pl, int64_t rows) {
+// Blocks of one wave.  Forward: 768 threads per SM of the small blocks, up to
+// 1024 of the larger; backward (more arithmetic, three reads to one write): 1024.
+int per_sm(const NormPlan& pl, bool backward) {
+  return std::max(1, (backward || pl.threads > 256 ? 1024 : 768) / pl.threads);
+}
+int blocks_for(const NormPlan& pl, int64_t rows, bool backward) {
   const int64_t need = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
-  const int64_t fit = static_cast<int64_t>(num_sms()) * std::max(1, 2048 / (pl.threads * pl.vpt));
-  return static_cast<int>(std::min(need, fit));
+  return static_cast<int>(std::min<int64_t>(need, static_cast<int64_t>(num_sms()) * per_sm(pl, backward)));
 }
 
-template <int VPT, bool WARP_ROW, bool MX>
+template <int VPT, bool WARP_ROW, bool MX, int DEPTH>
 gl_status run_fwd(const NormPlan& pl, int grid, const NormParams& p, cudaStream_t s) {
-  auto kern = rmsnorm_kernel<VPT, WARP_ROW, MX>;
-  const int smem = Ring<VPT, 2, kDepth>::bytes(pl.threads);
+  auto kern = rmsnorm_kernel<VPT, WARP_ROW, MX, DEPTH>;
+  const int smem = Ring<VPT, 2, DEPTH>::bytes(pl.threads);
   if (set_max_smem(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return GL_ERR_CUDA;
   kern<<<grid, pl.threads, smem, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? GL_OK : GL_ERR_CUDA;
 }
 
+// Two rows in flight per block, three where an SM holds one block only.
 template <bool MX>
 gl_status launch_fwd(const NormPlan& pl, int grid, const NormParams& p, cudaStream_t s) {
-  if (!pl.warp_row) return run_fwd<2, false, MX>(pl, grid, p, s);
-  if (pl.vpt == 1) return run_fwd<1, true, MX>(pl, grid, p, s);
-  return pl.vpt == 2 ? run_fwd<2, true, MX>(pl, grid, p, s) : run_fwd<4, true, MX>(pl, grid, p, s);
+  if (pl.warp_row) return run_fwd<1, true, MX, 2>(pl, grid, p, s);
+  if (pl.vpt == 2) return run_fwd<2, false, MX, 3>(pl, grid, p, s);
+  return per_sm(pl, false) > 1 ? run_fwd<1, false, MX, 2>(pl, grid, p, s) : run_fwd<1, false, MX, 3>(pl, grid, p, s);
 }
 
 template <int VPT, bool WARP_ROW>
 gl_status run_bwd(const NormPlan& pl, int grid, const NormBwdParams& p, cudaStream_t s) {
-  auto kern = rmsnorm_bwd_kernel<VPT, WARP_ROW>;
-  const int smem = Ring<VPT, 3, kBwdDepth>::bytes(pl.threads);
+  constexpr int kDepth = 2;
+  auto kern = rmsnorm_bwd_kernel<VPT, WARP_ROW, kDepth>;
+  const int smem = Ring<VPT, 3, kDepth>::bytes(pl.threads);
   if (set_max_smem(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return GL_ERR_CUDA;
   kern<<<grid, pl.threads, smem, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? GL_OK : GL_ERR_CUDA;
@@ -490,11 +496,11 @@ gl_status launch_rmsnorm(const void* x, const void* residual, const void* gamma,
                          cudaStream_t stream) {
   const NormPlan pl = plan_for(cols);
   NormParams p{x, residual, gamma, eps, rows, cols, sum, y, rstd, codes, scales, scale_layout == GL_SCALES_MMA};
-  const int grid = blocks_for(pl, rows);
+  const int grid = blocks_for(pl, rows, false);
   return codes != nullptr ? launch_fwd<true>(pl, grid, p, stream) : launch_fwd<false>(pl, grid, p, stream);
 }
 
-int64_t rmsnorm_bwd_blocks(int64_t rows, int cols) { return blocks_for(plan_for(cols), rows); }
+int64_t rmsnorm_bwd_blocks(int64_t rows, int cols) { return blocks_for(plan_for(cols), rows, true); }
 
 gl_status launch_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma, const float* rstd, const void* dsum,
                              int64_t rows, int cols, void* dx, float* dgamma, int accumulate, float* part,
@@ -503,10 +509,9 @@ gl_status launch_rmsnorm_bwd(const void* dy, const void* sum, const void* gamma,
   const int grid = static_cast<int>(rmsnorm_bwd_blocks(rows, cols));
   NormBwdParams p{dy, sum, gamma, rstd, dsum, rows, cols, dx, part};
   if (grid > 0) {
-    const gl_status st = !pl.warp_row     ? run_bwd<2, false>(pl, grid, p, stream)
-                         : pl.vpt == 1 ? run_bwd<1, true>(pl, grid, p, stream)
-                         : pl.vpt == 2 ? run_bwd<2, true>(pl, grid, p, stream)
-                                       : run_bwd<4, true>(pl, grid, p, stream);
+    const gl_status st = pl.warp_row ? run_bwd<1, true>(pl, grid, p, stream)
+                         : pl.vpt == 1 ? run_bwd<1, false>(pl, grid, p, stream)
+                                       : run_bwd<2, false>(pl, grid, p, stream);
     if (st != GL_OK) return st;
   }
   cudaLaunchConfig_t cfg = {};
