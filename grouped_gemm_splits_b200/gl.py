@@ -417,14 +417,14 @@ def _refuse(what: str, why: str) -> None:
     raise GlError(f"{what}: {why}")
 
 
-def _tensor(what: str, name: str, t, dtype, *shapes) -> None:
-    """Refuse anything but a contiguous tensor of this dtype and one of these shapes."""
+def _tensor(what: str, name: str, t, dtype, shape) -> None:
+    """Refuse anything but a contiguous tensor of this dtype and shape."""
     if not isinstance(t, torch.Tensor):
         _refuse(what, f"{name} must be a tensor")
     if t.dtype is not dtype:
         _refuse(what, f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape not in shapes:
-        _refuse(what, f"{name} must be {' or '.join(map(str, shapes))}, not {tuple(t.shape)}")
+    if t.shape != shape:
+        _refuse(what, f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         _refuse(what, f"{name} must be contiguous")
 
@@ -433,8 +433,14 @@ def _matrix(what: str, name: str, t) -> torch.Size:
     """The shape of a contiguous bf16 [rows, cols] tensor."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         _refuse(what, f"{name} must be a matrix")
-    _tensor(what, name, t, torch.bfloat16, t.shape)
-    return t.shape
+    shape = t.shape
+    _tensor(what, name, t, torch.bfloat16, shape)
+    return shape
+
+
+def _status_word(what: str, t) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.numel() != 1:
+        _refuse(what, "status must be one int32")
 
 
 class _On:
@@ -483,35 +489,41 @@ def gl_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optio
         _refuse(what, "at least one of y and mxfp8 is required")
     if mxfp8 and cols % (128 if mma_scales else 32):
         _refuse(what, f"cols = {cols} does not fit the scale layout")
-    given = out
-    want = [("rstd", torch.float32, (rows,))]
-    if residual is not None or (given and "sum" in given):
-        want.append(("sum", bf, shape))
-    if y:
-        want.append(("y", bf, shape))
-    if mxfp8:
-        want.append(("codes_r", torch.uint8, shape))
-        want.append(("scales_r", torch.uint8, ((rows + 127) // 128 * (cols // 128) * 512,) if mma_scales
-                     else (rows, cols // 32)))
-    out = {}
-    if given:
-        names = [w[0] for w in want]
-        for key in given:
-            if key not in names:
-                _refuse(what, f"out[{key!r}] is not an output of this call")
-    with _On(what, x, gamma, residual, *(given.values() if given else ())) as stream:
-        for key, dt, sh in want:
-            t = given.get(key) if given else None
-            if t is None:
-                t = torch.empty(sh, dtype=dt, device=x.device)
-            elif key == "scales_r":
-                _tensor(what, key, t, dt, sh, (rows * (cols // 32),) if not mma_scales else sh)
+    out = {} if out is None else dict(out)
+    with _On(what, x, gamma, residual, *out.values()) as stream:
+        rstd = out.get("rstd")
+        if rstd is None:
+            rstd = out["rstd"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+        else:
+            _tensor(what, "rstd", rstd, torch.float32, (rows,))
+        s = out.get("sum")
+        if s is not None:
+            _tensor(what, "sum", s, bf, shape)
+        elif residual is not None:
+            s = out["sum"] = torch.empty_like(x)
+        yt = out.get("y")
+        if yt is not None:
+            _tensor(what, "y", yt, bf, shape)
+        elif y:
+            yt = out["y"] = torch.empty_like(x)
+        codes, scales = out.get("codes_r"), out.get("scales_r")
+        if mxfp8:
+            if codes is None:
+                codes = out["codes_r"] = torch.empty_like(x, dtype=torch.uint8)
             else:
-                _tensor(what, key, t, dt, sh)
-            out[key] = t
-        _check(load().gl_rmsnorm(x.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, rows, cols,
-                                 _ptr(out.get("sum")), _ptr(out.get("y")), out["rstd"].data_ptr(),
-                                 _ptr(out.get("codes_r")), _ptr(out.get("scales_r")),
+                _tensor(what, "codes_r", codes, torch.uint8, shape)
+            size = ((rows + 127) // 128 * (cols // 128) * 512,) if mma_scales else (rows, cols // 32)
+            if scales is None:
+                scales = out["scales_r"] = torch.empty(size, dtype=torch.uint8, device=x.device)
+            elif mma_scales:
+                _tensor(what, "scales_r", scales, torch.uint8, size)
+            else:  # [rows, cols / 32], or the same bytes in a row
+                _tensor(what, "scales_r", scales, torch.uint8, size if scales.dim() == 2 else (rows * (cols // 32),))
+        known = 1 + (s is not None) + y + 2 * mxfp8
+        if len(out) != known:
+            _refuse(what, f"out has {sorted(out)}: more than this call's outputs")
+        _check(load().gl_rmsnorm(x.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, rows, cols, _ptr(s), _ptr(yt),
+                                 rstd.data_ptr(), _ptr(codes), _ptr(scales),
                                  GL_SCALES_MMA if mma_scales else GL_SCALES_ROWMAJOR, stream), what)
     return out
 
@@ -550,7 +562,7 @@ def gl_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, gamma: torch.Tensor, rst
         _refuse(what, "accumulate needs a dgamma")
     with _On(what, dy, sum, gamma, rstd, dsum, dx, dgamma, workspace) as stream:
         if dx is None:
-            dx = torch.empty(rows, cols, dtype=bf, device=dy.device)
+            dx = torch.empty_like(dy)
         if dgamma is None:
             dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
         if workspace is None:
@@ -567,15 +579,15 @@ def _gated(act: int) -> bool:
     return act in (GL_ACT_SWIGLU, GL_ACT_GEGLU)
 
 
-def _weights(what: str, name: str, w: TensorOrList, G: int, *shapes) -> torch.Tensor:
+def _weights(what: str, name: str, w: TensorOrList, G: int, shape) -> torch.Tensor:
     """Check a stacked tensor or a list of G tensors of the given per-group shape; returns one of them."""
     if isinstance(w, torch.Tensor):
-        _tensor(what, name, w, torch.bfloat16, *[(G, *s) for s in shapes])
+        _tensor(what, name, w, torch.bfloat16, (G, *shape))
         return w
     if len(w) != G:
         _refuse(what, f"{name} must have {G} tensors, not {len(w)}")
     for t in w:
-        _tensor(what, name, t, torch.bfloat16, *shapes)
+        _tensor(what, name, t, torch.bfloat16, shape)
         if t.device != w[0].device:
             _refuse(what, f"{name} on {w[0].device} and {t.device}")
     return w[0]
@@ -585,7 +597,7 @@ def _plan(what: str, offsets: torch.Tensor, status: torch.Tensor) -> int:
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
         _refuse(what, "offsets must be the [G + 1] tensor of gl_offsets")
     _tensor(what, "offsets", offsets, torch.int64, offsets.shape)
-    _tensor(what, "status", status, torch.int32, (1,), ())
+    _status_word(what, status)
     return offsets.numel() - 1
 
 
@@ -696,7 +708,7 @@ def gl_moe_tokens(x: torch.Tensor, w1: TensorOrList, w2: TensorOrList, top_k: in
     what = "gl_moe_tokens"
     bf = torch.bfloat16
     T, H = _matrix(what, "x", x)
-    _tensor(what, "status", status, torch.int32, (1,), ())
+    _status_word(what, status)
     E = len(w1)
     F = _shape_nk(w2)[1]
     a = _weights(what, "w1", w1, E, (2 * F, H))
@@ -719,7 +731,7 @@ def gl_moe_tokens(x: torch.Tensor, w1: TensorOrList, w2: TensorOrList, top_k: in
         if topk_w is None:
             topk_w = torch.empty(T, top_k, dtype=torch.float32, device=x.device)
         if y is None:
-            y = torch.empty(T, H, dtype=bf, device=x.device)
+            y = torch.empty_like(x)
         if workspace is None:
             workspace = torch.empty(moe_workspace_bytes(T, E, top_k, H, F), dtype=torch.uint8, device=x.device)
         g1, keep1 = _grouped(w1, E)
