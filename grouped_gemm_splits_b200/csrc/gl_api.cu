@@ -220,7 +220,7 @@ gl_status gl_fwd_act(const void* x, gl_grouped w, const gl_grouped* bias, const 
   c.M = M;
   c.N = N;
   c.K = K;
-  c.cta_pair = pair;
+  c.cta_pair = opts == nullptr ? -1 : pair;
   c.wait_ns = wait_ns;
   c.hold_loads = hold;
   c.stream = to_stream(stream);
@@ -260,7 +260,7 @@ gl_status gl_dgrad_act(const void* dy, gl_grouped w, const void* z, int act, con
   c.M = M;
   c.N = N;
   c.K = K;
-  c.cta_pair = pair;
+  c.cta_pair = opts == nullptr ? -1 : pair;
   c.wait_ns = wait_ns;
   c.hold_loads = hold;
   c.stream = to_stream(stream);

@@ -978,9 +978,34 @@ gl_status launch_cg(const GemmCall& c) {
   return c.cta_pair ? launch_mode<MODE, 2, EPI>(c) : launch_mode<MODE, 1, EPI>(c);
 }
 
+// Tile shape of the epilogue forms where the caller leaves it open: 256-row
+// tiles on pairs, or 128-row tiles on single CTAs, which pad short groups less
+// and fill the last wave better but read twice as much of W per row.  The split
+// sizes are on the device, so the groups are taken to end half a tile in; a
+// wave of single tiles is taken to last 1.18 of a wave of pairs.  Measured,
+// pairs against singles, 64 groups of 2048 x 2816 swiglu: 32768 rows 385 / 396
+// us, 24576 314 / 327, 16384 252 / 234, 2048 154 / 125; 8 groups of 14336 x 4096:
+// 8192 rows 802 / 907, 4096 474 / 437, 1024 238 / 264, 512 231 / 170 (of ten
+// such points the rule missed one, by 11%).
+bool pairs_fit_better(const GemmCall& c) {
+  const bool gated = act_gated(c.act);
+  const int64_t cols = c.mode == kFwd ? (gated ? (c.N / 2 + 127) / 128 : (c.N + 255) / 256) : (c.K + 255) / 256;
+  auto waves = [&](int64_t rows, int64_t units) {
+    const int64_t row_tiles = std::max<int64_t>(std::min<int64_t>(c.G, c.M), c.M / rows + c.G / 2);
+    return (row_tiles * cols + units - 1) / units;
+  };
+  const int64_t sms = std::max(2, num_sms());
+  return waves(256, sms / 2) * 100 <= waves(128, sms) * 118;
+}
+
 }  // namespace
 
 gl_status launch_grouped_gemm(const GemmCall& c) {
+  if (c.cta_pair < 0) {
+    GemmCall chosen = c;
+    chosen.cta_pair = pairs_fit_better(c) ? 1 : 0;
+    return launch_grouped_gemm(chosen);
+  }
   if (c.epilogue) {
     const bool gated = act_gated(c.act);
     if (c.mode == kFwd) return gated ? launch_cg<kFwd, kEpiGated>(c) : launch_cg<kFwd, kEpiAct>(c);

@@ -39,7 +39,7 @@ struct GemmCall {
   int64_t M;
   int N, K;
   int accumulate;
-  int cta_pair;  // 1: 256x256 tiles on CTA pairs (cta_group::2); 0: 128x256 tiles per CTA
+  int cta_pair;  // 1: 256x256 tiles on CTA pairs (cta_group::2); 0: 128x256 tiles per CTA; -1: chosen by size
   uint64_t wait_ns;  // bound on each pipeline wait inside the kernel
   int hold_loads;    // testing: issue no loads (every pipeline wait runs out)
   cudaStream_t stream;

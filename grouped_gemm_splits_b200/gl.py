@@ -157,6 +157,13 @@ def _opts(pair: bool, wait_limit_us: int, flags: int = 0):
     return ctypes.pointer(GlGemmOpts(GL_TILES_PAIR if pair else GL_TILES_SINGLE, wait_limit_us, flags))
 
 
+def _opts_open(pair: Optional[bool], wait_limit_us: int, flags: int):
+    """The same where None for ``pair`` leaves the tile shape to the library."""
+    if pair is None and not wait_limit_us and not flags:
+        return None
+    return ctypes.pointer(GlGemmOpts(GL_TILES_SINGLE if pair is False else GL_TILES_PAIR, wait_limit_us, flags))
+
+
 def gl_offsets(m_splits: torch.Tensor, expect_rows: int, out_rows: Optional[int] = None,
                offsets: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
     """Device prefix scan of ``m_splits`` (int64[G]) -> (offsets int64[G+1], status int32[1])."""
@@ -609,13 +616,14 @@ def _rows_at_least(what: str, name: str, t: torch.Tensor, rows: int, cols: int) 
 
 def gl_fwd_act(x: torch.Tensor, w: TensorOrList, bias: Optional[TensorOrList], offsets: torch.Tensor,
                status: torch.Tensor, act: int, residual: Optional[torch.Tensor] = None, save_z: bool = False,
-               z: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, pair: bool = True,
+               z: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, pair: Optional[bool] = None,
                wait_limit_us: int = 0, opt_flags: int = 0):
     """:func:`gl_fwd` with an activation (``GL_ACT_*``) and a residual in its
     epilogue: y = act(x W^T + b) + residual, or, gated, act(u0) * u1 + residual
     on the halves of u = x W^T + b.  Returns (y, z): z is u (bf16 [M, N]), what
     :func:`gl_dgrad_act` reads, if ``save_z`` is set or a ``z`` is given, else
     None.  ``y`` may have more rows than x; only the valid ones are written.
+    ``pair`` picks the tile shape (None: by size).
     """
     what = "gl_fwd_act"
     G = _plan(what, offsets, status)
@@ -645,14 +653,14 @@ def gl_fwd_act(x: torch.Tensor, w: TensorOrList, bias: Optional[TensorOrList], o
             bg, keep_b = _grouped(bias, G)
             bptr = ctypes.pointer(bg)
         _check(load().gl_fwd_act(x.data_ptr(), wg, bptr, _ptr(residual), act, offsets.data_ptr(), status.data_ptr(),
-                                 G, M, N, K, _ptr(z), y.data_ptr(), y.shape[0], _opts(pair, wait_limit_us, opt_flags),
+                                 G, M, N, K, _ptr(z), y.data_ptr(), y.shape[0], _opts_open(pair, wait_limit_us, opt_flags),
                                  stream), what)
     del keep_w, keep_b
     return y, z
 
 
 def gl_dgrad_act(dy: torch.Tensor, w: TensorOrList, z: torch.Tensor, offsets: torch.Tensor, status: torch.Tensor,
-                 act: int, dz: Optional[torch.Tensor] = None, pair: bool = True, wait_limit_us: int = 0,
+                 act: int, dz: Optional[torch.Tensor] = None, pair: Optional[bool] = None, wait_limit_us: int = 0,
                  opt_flags: int = 0) -> torch.Tensor:
     """:func:`gl_dgrad` that goes on through the activation in front of the
     product: dz = (dy W) * act'(z), with z from the :func:`gl_fwd_act` before
@@ -674,7 +682,7 @@ def gl_dgrad_act(dy: torch.Tensor, w: TensorOrList, z: torch.Tensor, offsets: to
             dz = torch.empty(M, width, dtype=torch.bfloat16, device=dy.device)
         wg, keep = _grouped(w, G)
         _check(load().gl_dgrad_act(dy.data_ptr(), wg, z.data_ptr(), act, offsets.data_ptr(), status.data_ptr(), G, M,
-                                   N, K, dz.data_ptr(), dz.shape[0], _opts(pair, wait_limit_us, opt_flags), stream),
+                                   N, K, dz.data_ptr(), dz.shape[0], _opts_open(pair, wait_limit_us, opt_flags), stream),
                what)
     del keep
     return dz

@@ -399,8 +399,10 @@ gl_status gl_wgrad_mxfp8(const uint8_t* x_codes_c, const uint8_t* x_scales_c, co
  * residual stream.  Everything past the product is computed on the fp32
  * accumulator; each output is rounded once.
  *
- *   x, w, bias, offsets, status, opts   as for gl_fwd; w [N, K] of a gated
+ *   x, w, bias, offsets, status   as for gl_fwd; w [N, K] of a gated
  *             activation holds the F rows of the activated factor first
+ *   opts      as for gl_fwd, but NULL leaves the tile shape to the library,
+ *             which chooses by M, G and the widths (short groups: single CTAs)
  *   residual  NULL or device bf16 [M, columns of y]
  *   act       GL_ACT_*
  *   z         NULL or device bf16 [M, N], written: u, which gl_dgrad_act of
@@ -431,7 +433,7 @@ gl_status gl_fwd_act(const void* x, gl_grouped w, const gl_grouped* bias, const 
  * (for gl_dgrad, gl_wgrad and gl_dbias).  The gradient of a residual added by
  * gl_fwd_act is its dy, unchanged.
  *
- *   dy, w, offsets, status, opts   as for gl_dgrad
+ *   dy, w, offsets, status   as for gl_dgrad; opts as for gl_fwd_act
  *   act      GL_ACT_RELU .. GL_ACT_GEGLU (GL_ACT_NONE is gl_dgrad)
  *   z        device bf16 [M, K] ([M, 2K] when gated)
  *   dz       device bf16 [dz_rows, K] ([dz_rows, 2K]), dz_rows >= M; rows

@@ -52,7 +52,7 @@ CASES = [  # splits, K, N
 
 @pytest.mark.parametrize("m,K,N", CASES)
 @pytest.mark.parametrize("name", blk.ACTS)
-@pytest.mark.parametrize("bias,residual,pair", [(False, False, True), (True, True, True), (True, True, False)])
+@pytest.mark.parametrize("bias,residual,pair", [(False, False, None), (True, True, True), (True, True, False)])
 def test_forward(m, K, N, name, bias, residual, pair):
     G, M = len(m), sum(m)
     x, w = _rand(M, K, seed=1), _rand(G, N, K, seed=2, std=2.0 / np.sqrt(K))
