@@ -9,7 +9,7 @@
 //
 // Bound by HBM: every expert that some token reaches has its 3 H F weights
 // read once, whatever T (up to 128) is.  So the weights are the M operand of
-// the tensor-core products (tiles of 128 weight rows x 64 contraction
+// the tensor-core products (tiles of 128 weight rows x 128 contraction
 // elements, streamed by TMA through a deep ring) and the tokens are the N
 // operand (16 .. 128 columns).
 //
@@ -445,9 +445,15 @@ int route_smem(int T, int E, int k, bool router) {
 
 // ------------------------------------------------------------------- experts
 constexpr int kThreads = 256;  // warps: 0 weights, 1 tokens / h, 2 MMA, 3 -, 4-7 epilogue
-constexpr int kABytes = 128 * 64 * 2;
+// A block is 128 weight rows x 128 contraction elements (two boxes of one
+// 128-byte swizzle row): the MMA thread spends some 0.2 us per block on its
+// barriers, so blocks of 64 elements held it above what HBM delivers.
+constexpr int kBK = 128;
+constexpr int kABytes = 128 * kBK * 2;
+constexpr int kHalf = kABytes / 2;  // one 64-element box of it
 constexpr int kChunk = 16;     // slots per epilogue step
-constexpr int kMaxStages = 11;
+constexpr int kMaxStages = 5;  // 160 KB of weights in flight: with six the SMs' shares of HBM drift apart
+// (8 experts of 4096 x 14336, one token: 125 against 122 us), with three they wait (127)
 constexpr int kBarBytes = 256;
 constexpr int kExBytes = kChunk * 64 * 4;
 
@@ -513,7 +519,7 @@ __device__ __forceinline__ Phase make_phase(int n_act, int tiles, int kb, int ct
 // Whether the W1 tiles are better left whole: the slowest CTA's extra blocks
 // against the exchange of a cut tile's partials (two trips through L2 and an
 // atomic, about as long as kCutBlocks blocks take to stream).
-constexpr int kCutBlocks = 8;
+constexpr int kCutBlocks = 4;
 __device__ __forceinline__ bool keep_whole(int units, int kb, int ctas) {
   const int64_t most = static_cast<int64_t>((units + ctas - 1) / ctas) * kb;
   return most <= static_cast<int64_t>(units) * kb / ctas + kCutBlocks;
@@ -608,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     experts_kernel(const __grid_constant__ ExpertParams p, const __grid_constant__ ExpertMaps<PG> pg) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int stage_bytes = kABytes + p.nt * 128;
+  const int stage_bytes = kABytes + p.nt * kBK * 2;
   uint8_t* tail = smem + p.stages * stage_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);
   uint64_t* empty = full + kMaxStages;
@@ -669,9 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int ctas = static_cast<int>(gridDim.x);
-  const int tiles1 = (p.F + 63) / 64, kb1 = (p.H + 63) / 64;
+  const int tiles1 = (p.F + 63) / 64, kb1 = (p.H + kBK - 1) / kBK;
   const Phase f1 = make_phase(n_act, tiles1, kb1, ctas, keep_whole(n_act * tiles1, kb1, ctas));
-  const Phase f2 = make_phase(n_act, (p.H + 127) / 128, (p.F + 63) / 64, ctas, false);
+  const Phase f2 = make_phase(n_act, (p.H + 127) / 128, (p.F + kBK - 1) / kBK, ctas, false);
 
   // Before a producer leaves: wait for its last copies to land (the stage also
   // waits for the other producer, which may have given up: one bound for all).
@@ -712,12 +718,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       walk(f1, [&](uint8_t* dst, uint64_t* bar, int e, int tile, int kb) {
         const CUtensorMap* m = PG ? pg.m1(e) : &p.w1;
         const int z = PG ? 0 : 2 * e;
-        tma_load_3d_hint(dst, m, bar, kb * 64, tile * 64, z, policy);
-        tma_load_3d_hint(dst + kABytes / 2, m, bar, kb * 64, tile * 64, z + 1, policy);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tma_load_3d_hint(dst + c * kHalf, m, bar, kb * kBK + c * 64, tile * 64, z, policy);
+          tma_load_3d_hint(dst + c * kHalf + kHalf / 2, m, bar, kb * kBK + c * 64, tile * 64, z + 1, policy);
+        }
       });
       if (!*abort_flag)
         walk(f2, [&](uint8_t* dst, uint64_t* bar, int e, int tile, int kb) {
-          tma_load_3d_hint(dst, PG ? pg.m2(e) : &p.w2, bar, kb * 64, tile * 128, PG ? 0 : e, policy);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            tma_load_3d_hint(dst + c * kHalf, PG ? pg.m2(e) : &p.w2, bar, kb * kBK + c * 64, tile * 128, PG ? 0 : e, policy);
         });
       drain(stage, phase, issued);
     }
@@ -747,11 +758,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint8_t* dst = smem + stage * stage_bytes + kABytes;
             if (!p.hold_loads) {
-              mbar_arrive_expect_tx(&full[stage], rows * 128);
-              if (!second) {
-                tma_load_2d(dst, &p.x, &full[stage], kb * 64, 0);
-              } else {
-                for (int r = 0; r < rows; r += 16) tma_load_2d(dst + r * 128, &p.h, &full[stage], kb * 64, off + r);
+              mbar_arrive_expect_tx(&full[stage], rows * kBK * 2);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint8_t* to = dst + c * p.nt * 128;
+                if (!second) {
+                  tma_load_2d(to, &p.x, &full[stage], kb * kBK + c * 64, 0);
+                } else {
+                  for (int r = 0; r < rows; r += 16)
+                    tma_load_2d(to + r * 128, &p.h, &full[stage], kb * kBK + c * 64, off + r);
+                }
               }
             }
             ++issued;
@@ -765,45 +781,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     // ===================== MMA =====================
-    int stage = 0, it = 0;
-    uint32_t phase = 0;
-    auto walk = [&](const Phase& f, bool second) {
-      return for_segments(f, cta, [&](const Segment& s) {
-        const int n = second ? ceil16(act_off[s.j + 1] - act_off[s.j]) : p.nt;
-        const uint32_t idesc = idesc_bf16_f32(128, n, 0, 0);
-        const int buf = it & 1;
-        const uint32_t tph = (it >> 1) & 1;
-        ++it;
-        if (!__all_sync(0xffffffffu, mbar_wait(&tempty[buf], tph ^ 1u, abort_flag, p.wait_ns))) {
-          report_abort(abort_flag, p.status);
-          return false;
-        }
-        tc_fence_after();
-        for (int kb = s.lo; kb < s.hi; ++kb) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, p.wait_ns))) {
+    // One thread waits, issues and commits: with the whole warp at the barriers
+    // a block took 0.37 us, as long as it takes to stream from HBM.
+    if (lane == 0) {
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      auto walk = [&](const Phase& f, bool second) {
+        return for_segments(f, cta, [&](const Segment& s) {
+          const int n = second ? ceil16(act_off[s.j + 1] - act_off[s.j]) : p.nt;
+          const uint32_t idesc = idesc_bf16_f32(128, n, 0, 0);
+          const int buf = it & 1;
+          const uint32_t tph = (it >> 1) & 1;
+          ++it;
+          if (!mbar_wait(&tempty[buf], tph ^ 1u, abort_flag, p.wait_ns)) {
             report_abort(abort_flag, p.status);
             return false;
           }
           tc_fence_after();
-          if (lane == 0) {
+          for (int kb = s.lo; kb < s.hi; ++kb) {
+            if (!mbar_wait(&full[stage], phase, abort_flag, p.wait_ns)) {
+              report_abort(abort_flag, p.status);
+              return false;
+            }
+            tc_fence_after();
             const uint32_t sa = smem_u32(smem + stage * stage_bytes);
             const uint64_t ad = smem_desc_sw128(sa, 16, 1024);
             const uint64_t bd = smem_desc_sw128(sa + kABytes, 16, 1024);
+            const uint32_t b_half = static_cast<uint32_t>(p.nt) * 8;  // 16-byte units of one box of tokens
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ss(tmem_base + buf * 128, desc_add(ad, ks * 2), desc_add(bd, ks * 2), idesc,
-                          (kb > s.lo || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ss(tmem_base + buf * 128, desc_add(ad, (ks >> 2) * (kHalf / 16) + (ks & 3) * 2),
+                          desc_add(bd, (ks >> 2) * b_half + (ks & 3) * 2), idesc, (kb > s.lo || ks > 0) ? 1u : 0u);
             tc_commit(&empty[stage]);
             if (kb == s.hi - 1) tc_commit(&tfull[buf]);
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
           }
-          __syncwarp();
-          if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-        }
-        return true;
-      });
-    };
-    if (walk(f1, false)) walk(f2, true);
-    if (lane == 0) {
+          return true;
+        });
+      };
+      if (walk(f1, false)) walk(f2, true);
       tc_commit(mma_done);
       mbar_wait_bounded(mma_done, 0);  // no MMA in flight past this point
     }
@@ -1083,7 +1099,7 @@ gl_status launch_moe(const MoeCall& c) {
   p.F = c.F;
   p.act = act_inner(c.act);
   p.nt = ceil16(c.T);
-  const int stage_bytes = kABytes + p.nt * 128;
+  const int stage_bytes = kABytes + p.nt * kBK * 2;
   p.stages = std::min(kMaxStages, (232448 - 1024 - kTailBytes) / stage_bytes);
   p.wait_ns = c.wait_ns ? c.wait_ns : kWaitLimitNs;
   p.hold_loads = c.hold_loads;
