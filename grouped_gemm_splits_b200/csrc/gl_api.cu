@@ -201,7 +201,8 @@ gl_status gl_fwd_act(const void* x, gl_grouped w, const gl_grouped* bias, const 
     return GL_ERR_INVALID;
   if (!grouped_ok(w, G) || (bias != nullptr && !grouped_ok(*bias, G))) return GL_ERR_INVALID;
   if (y_rows < M) return GL_ERR_INVALID;
-  if (M > 0 && z != nullptr && (z == y || z == residual)) return GL_ERR_INVALID;
+  // y and z are written while other tiles still read x; z is not the residual's buffer
+  if (M > 0 && (y == x || (z != nullptr && (z == y || z == residual || z == x)))) return GL_ERR_INVALID;
   if (gl::act_gated(act) && N % 16 != 0) return GL_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(y) || !aligned16(z) || !aligned16(residual) || !grouped_aligned(w, G) ||
       (bias && !grouped_aligned(*bias, G)))
@@ -244,7 +245,7 @@ gl_status gl_dgrad_act(const void* dy, gl_grouped w, const void* z, int act, con
     return GL_ERR_INVALID;
   if (!grouped_ok(w, G)) return GL_ERR_INVALID;
   if (dz_rows < M) return GL_ERR_INVALID;
-  if (M > 0 && z == dz) return GL_ERR_INVALID;
+  if (M > 0 && (dz == z || dz == dy)) return GL_ERR_INVALID;
   if (gl::act_gated(act) && K > (1 << 30)) return GL_ERR_UNSUPPORTED;  // 2K columns of z
   if (!aligned16(dy) || !aligned16(z) || !aligned16(dz) || !grouped_aligned(w, G)) return GL_ERR_UNSUPPORTED;
   if (M == 0) return GL_OK;

@@ -409,7 +409,7 @@ gl_status gl_wgrad_mxfp8(const uint8_t* x_codes_c, const uint8_t* x_scales_c, co
  *             the next product reads
  *   y         device bf16 [y_rows, N] ([y_rows, F] when gated), y_rows >= M;
  *             rows [M, y_rows) are not written; may be the same buffer as
- *             residual
+ *             residual, not as x or z
  * Limits: those of gl_fwd, and N % 16 == 0 when gated.
  */
 #define GL_ACT_NONE 0
@@ -437,7 +437,7 @@ gl_status gl_fwd_act(const void* x, gl_grouped w, const gl_grouped* bias, const 
  *   act      GL_ACT_RELU .. GL_ACT_GEGLU (GL_ACT_NONE is gl_dgrad)
  *   z        device bf16 [M, K] ([M, 2K] when gated)
  *   dz       device bf16 [dz_rows, K] ([dz_rows, 2K]), dz_rows >= M; rows
- *            [M, dz_rows) are not written; not the same buffer as z
+ *            [M, dz_rows) are not written; not the same buffer as z or dy
  * relu's slope at 0 is 0.  Limits: those of gl_dgrad.
  */
 gl_status gl_dgrad_act(const void* dy, gl_grouped w, const void* z, int act, const int64_t* offsets,
@@ -500,7 +500,8 @@ gl_status gl_rmsnorm(const void* x, const void* residual, const void* gamma, flo
  *   dgamma     device fp32 [cols]: accumulate != 0 adds to it, 0 overwrites
  *   workspace  device scratch of workspace_bytes >=
  *              gl_rmsnorm_bwd_workspace_bytes(rows, cols), 256-byte aligned;
- *              its contents on entry do not matter
+ *              its contents on entry do not matter; calls that can overlap on
+ *              the GPU need one each
  * The size of the workspace follows the current device's SM count.  Limits
  * as for gl_rmsnorm; two launches.  rows == 0 writes zeros to dgamma when it
  * overwrites.

@@ -18,7 +18,7 @@ def _d(dy=16, w=W, z=16, act=3, off=16, st=16, G=2, M=8, N=32, K=16, dz=32, rows
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(w=NOW), dict(off=None), dict(st=None), dict(y=None), dict(rows=7),
                                 dict(G=0), dict(G=4097), dict(N=0), dict(act=-1), dict(act=7), dict(z=32),
-                                dict(z=48, res=48)])
+                                dict(z=48, res=48), dict(z=16), dict(y=16)])
 def test_forward_invalid(kw):
     assert _f(**kw) == gl.GL_ERR_INVALID
 
@@ -30,7 +30,7 @@ def test_forward_unsupported(kw):
 
 
 @pytest.mark.parametrize("kw", [dict(dy=None), dict(w=NOW), dict(z=None), dict(off=None), dict(st=None), dict(dz=None),
-                                dict(rows=7), dict(act=0), dict(act=7), dict(z=32), dict(G=0)])
+                                dict(rows=7), dict(act=0), dict(act=7), dict(z=32), dict(dy=32), dict(G=0)])
 def test_gradient_invalid(kw):
     assert _d(**kw) == gl.GL_ERR_INVALID
 

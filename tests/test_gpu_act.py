@@ -261,3 +261,24 @@ def test_captured_and_replayed_on_another_stream():
         graph.replay()
         want_y, want_z = step()
         assert torch.equal(y, want_y) and torch.equal(z, want_z)
+
+
+def test_more_than_two_to_the_31_elements():
+    """Offsets past 32 bits: the last rows of y and z, 300000 x 8192 and 300000 x 16384."""
+    M, K, F, last = 300000, 16, 8192, 4
+    x, w = torch.zeros(M, K, dtype=BF, device="cuda"), _rand(2, 2 * F, K, seed=1)
+    x[-last:] = _rand(last, K, seed=2)
+    off, st = offsets_on_device([M - 3, 3], M)
+    y, z = gl.gl_fwd_act(x, w, None, off, st, gl.GL_ACT_SWIGLU, save_z=True)
+    m = [last - 3, 3]
+    ref, u = blk.fwd_act(f64(x[-last:]), f64(w), None, m, "swiglu", None)
+    assert orc.rel_frobenius(f64(y[-last:]), ref) <= 5e-3 and orc.rel_frobenius(f64(z[-last:]), u) <= 5e-3
+    assert not y[:last].any() and not z[:last].any()
+    del y
+    z[:-last] = 0
+    dy = torch.zeros(M, K, dtype=BF, device="cuda")
+    dy[-last:] = _rand(last, K, seed=3)
+    w2 = _rand(2, K, F, seed=4)
+    dz = gl.gl_dgrad_act(dy, w2, z, off, st, gl.GL_ACT_SWIGLU)
+    assert orc.rel_frobenius(f64(dz[-last:]), blk.dgrad_act(f64(dy[-last:]), f64(w2), m, "swiglu", f64(z[-last:]))) <= 5e-3
+    assert not dz[:last].any() and int(st.item()) == 0

@@ -252,3 +252,43 @@ def test_captured_and_replayed_and_two_streams():
         want = gl.gl_moe_tokens(v, w1, w2, k, st, router_w=router)[0]
         assert all(torch.equal(want, o) for o in got)
     assert int(st.item()) == 0
+
+
+def test_decoding_steps_of_two_blocks():
+    """Norm with the residual's addition -> router and experts, twice, captured as a decoding step and replayed,
+    against the oracle (which follows the experts that the call reports, up to near ties of bf16 inputs)."""
+    T, E, k, H, F = 3, 16, 4, 256, 192
+    layers = [(_rand(H, seed=i, std=0.1) + 1, _layer(T, E, H, F, seed=10 * i)[1:]) for i in (1, 2)]
+    x, st = _rand(T, H, seed=5), _status()
+    zero = torch.zeros_like(x)
+
+    def step():
+        add, res, kept = zero, x, []
+        for gamma, (router, w1, w2) in layers:
+            n = gl.gl_rmsnorm(add, gamma, 1e-5, residual=res)
+            add, idx, w = gl.gl_moe_tokens(n["y"], w1, w2, k, st, router_w=router)
+            res = n["sum"]
+            kept.append((n["y"], idx, w, add))
+        return kept, gl.gl_rmsnorm(add, layers[0][0], 1e-5, residual=res)["sum"]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept, out = step()
+    for seed in (21, 22):
+        x.copy_(_rand(T, H, seed=seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        stream = f64(x)
+        for (gamma, (router, w1, w2)), (n, idx, w, y) in zip(layers, kept):
+            _, _, norm = blk.rmsnorm(stream, None, f64(gamma), 1e-5)
+            assert orc.rel_frobenius(f64(n), norm) <= TOL_BF16
+            i, ww = _check_route(idx, w, n, router, k, True)
+            _check_y(y, n, i, ww, w1, w2, "swiglu")
+            stream = stream + blk.experts(norm, i, ww, f64(w1), f64(w2), "swiglu")
+        assert orc.rel_frobenius(f64(out), stream) <= 1e-2

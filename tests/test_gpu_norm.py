@@ -202,3 +202,46 @@ def test_forward_output_feeds_the_mxfp8_product_and_graph_replay():
     nd = orc.dequant_rowwise(nq, ns)
     ref[:100], ref[100:] = nd[:100] @ wd[0].T, nd[100:] @ wd[2].T
     assert orc.rel_frobenius(f64(y), ref) <= 1e-2
+
+
+def test_backward_captured_and_replayed():
+    """Two captured backward passes in one graph, each with its own workspace, follow new inputs."""
+    rows, cols = 700, 1040
+    s, dy, gamma = _rand(rows, cols, seed=1), _rand(rows, cols, seed=2), _rand(cols, seed=3, mean=1.0)
+    rstd = torch.rsqrt(s.float().square().mean(1) + EPS)
+    dg = torch.zeros(cols, device="cuda")
+
+    def step(dg):
+        dx, _ = gl.gl_rmsnorm_bwd(dy, s, gamma, rstd, dgamma=dg, accumulate=True)
+        return gl.gl_rmsnorm_bwd(dx, s, gamma, rstd, dsum=dy, dgamma=dg, accumulate=True)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(torch.zeros_like(dg))
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(dg)
+    total = torch.zeros_like(dg)
+    for seed in (7, 8):
+        dy.copy_(_rand(rows, cols, seed=seed))
+        graph.replay()
+        assert torch.equal(out, step(total)) and torch.equal(dg, total)
+
+
+def test_more_than_two_to_the_31_elements():
+    """Offsets past 32 bits: the last rows of 300000 x 8192 (4.9 GB a tensor)."""
+    rows, cols, last = 300000, 8192, 5
+    x, gamma = torch.zeros(rows, cols, dtype=BF, device="cuda"), _rand(cols, seed=3, mean=1.0)
+    x[-last:] = _rand(last, cols, seed=1)
+    out = gl.gl_rmsnorm(x, gamma, EPS, mxfp8=True)
+    s, rstd, y = blk.rmsnorm(f64(x[-last:]), None, f64(gamma), EPS)
+    _close_bf16(out["y"][-last:], y)
+    _check_codes(out["codes_r"][-last:], out["scales_r"][-last:], y, False)
+    assert not out["y"][:last].any()
+    del out["codes_r"]
+    dx, dg = gl.gl_rmsnorm_bwd(x, x, gamma, out["rstd"], dx=out["y"])
+    rdx, _ = blk.rmsnorm_bwd(s, s, f64(gamma), f64(out["rstd"][-last:]), None)
+    assert orc.rel_frobenius(f64(dx[-last:]), rdx) <= 5e-3
+    assert not dx[:last].any()
