@@ -64,7 +64,7 @@ gl_status check_gemm_dims(int G, int64_t M, int N, int K) {
 
 extern "C" {
 
-int gl_version(void) { return 200; }
+int gl_version(void) { return 300; }
 
 const char* gl_status_string(gl_status s) {
   switch (s) {

@@ -147,7 +147,11 @@ __host__ __device__ __forceinline__ RouteSplit route_split(int T, int E) {
 // Logits of all tokens over this CTA's part of H into part[ks][T][E].  A
 // thread takes 8 consecutive elements of its expert row and of its token row
 // and uses them as the k pairs of two MMAs: the order of a contraction is
-// free, as long as both operands share it.
+// free, as long as both operands share it.  TILES: token tiles of 8 per unit;
+// the fewer there are, the more of the slice is loaded at once (a warp's chain
+// of loads is what this takes: one token over 128 experts of 7168 x 2048 ran
+// 133 us with four tiles and two steps at once, 129 us with one and four).
+template <int TILES, int UNROLL>
 __device__ __forceinline__ void route_logits(const RouteParams& p, const RouteSplit& sp, float* part, int rank, int warp,
                                              int lane) {
   const int g = lane >> 2, t4 = lane & 3;
@@ -161,35 +165,32 @@ __device__ __forceinline__ void route_logits(const RouteParams& p, const RouteSp
     const bool r0 = e0 + g < p.E, r1 = e0 + g + 8 < p.E;
     const __nv_bfloat16* w0 = p.router + static_cast<int64_t>(e0 + g) * p.H;
     const __nv_bfloat16* w1 = w0 + static_cast<int64_t>(8) * p.H;
-    float c[4][4] = {};
-    const int tiles = min(4, (p.T - n0 + 7) >> 3);
-#pragma unroll 2
+    float c[TILES][4] = {};
+#pragma unroll UNROLL
     for (int kk = k0 + t4 * 8; kk - t4 * 8 < k1; kk += 32) {
       const bool in = kk < k1;
       const uint4 a = (in && r0) ? __ldg(reinterpret_cast<const uint4*>(w0 + kk)) : zero;
       const uint4 b = (in && r1) ? __ldg(reinterpret_cast<const uint4*>(w1 + kk)) : zero;
-      uint4 v[4];
+      uint4 v[TILES];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < TILES; ++j) {
         const int t = n0 + j * 8 + g;
         v[j] = (in && t < p.T) ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.H + kk)) : zero;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j < tiles) {
-          mma_16816(c[j], a.x, b.x, a.y, b.y, v[j].x, v[j].y);
-          mma_16816(c[j], a.z, b.z, a.w, b.w, v[j].z, v[j].w);
-        }
+      for (int j = 0; j < TILES; ++j) {
+        mma_16816(c[j], a.x, b.x, a.y, b.y, v[j].x, v[j].y);
+        mma_16816(c[j], a.z, b.z, a.w, b.w, v[j].z, v[j].w);
       }
     }
     float* dst = part + ks * p.T * p.E;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < TILES; ++j) {
       const int t = n0 + j * 8 + t4 * 2;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tt = t + (i & 1), e = e0 + g + (i >> 1) * 8;
-        if (j < tiles && tt < p.T && e < p.E) dst[tt * p.E + e] = c[j][i];
+        if (tt < p.T && e < p.E) dst[tt * p.E + e] = c[j][i];
       }
     }
   }
@@ -289,7 +290,8 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __maxnreg__(80)
   }
   if (p.router != nullptr) {
     const RouteSplit sp = route_split(p.T, p.E);
-    route_logits(p, sp, part, rank, warp, lane);
+    if (p.T <= 8) route_logits<1, 4>(p, sp, part, rank, warp, lane);
+    else route_logits<4, 2>(p, sp, part, rank, warp, lane);
     if (sp.ks > 1) {
       __syncthreads();
       for (int i = tid; i < p.T * p.E; i += kRouteThreads) {
