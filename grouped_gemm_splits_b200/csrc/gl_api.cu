@@ -602,7 +602,7 @@ gl_status gl_moe_tokens(const void* x, const void* router, gl_grouped w1, gl_gro
   if (!grouped_ok(w1, E) || !grouped_ok(w2, E) || status == nullptr || workspace == nullptr) return GL_ERR_INVALID;
   if (T > 0 && (x == nullptr || topk_idx == nullptr || topk_w == nullptr || y == nullptr)) return GL_ERR_INVALID;
   if (workspace_bytes < gl_moe_workspace_bytes(T, E, top_k, H, F)) return GL_ERR_INVALID;
-  if ((w1.mode != GL_STACKED || w2.mode != GL_STACKED) && E > 64) return GL_ERR_UNSUPPORTED;
+  if ((w1.mode != GL_STACKED || w2.mode != GL_STACKED) && E > GL_MOE_MAX_PER_GROUP) return GL_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(router) || !aligned16(y) || !grouped_aligned(w1, E) || !grouped_aligned(w2, E) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) || (reinterpret_cast<uintptr_t>(topk_idx) & 3u) ||
       (reinterpret_cast<uintptr_t>(topk_w) & 3u))

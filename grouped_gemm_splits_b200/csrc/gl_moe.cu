@@ -57,7 +57,7 @@ constexpr int kMaxT = GL_MOE_MAX_TOKENS;
 constexpr int kMaxE = GL_MOE_MAX_EXPERTS;
 constexpr int kMaxSlots = GL_MOE_MAX_TOKENS * GL_MOE_MAX_TOP_K;
 constexpr int kMaxCtas = 256;  // counters are laid out for up to this many CTAs
-constexpr int kPG = 64;        // per-expert tensor maps carried by a launch
+constexpr int kPG = GL_MOE_MAX_PER_GROUP;  // experts whose tensor maps a launch carries (32 KB of parameters)
 
 // ------------------------------------------------------------- the workspace
 // Counters (cleared by route_kernel) and the plan (written by it).

@@ -549,13 +549,14 @@ size_t gl_rmsnorm_bwd_workspace_bytes(int64_t rows, int cols);
  *             matter.  Calls that can overlap on the GPU need one each.
  *   opts      NULL or per-call options (tiles must be GL_TILES_PAIR, the default)
  * A token whose logits hold a NaN gets NaN weights and a NaN y.
- * Limits: H % 8 == 0, F % 8 == 0, E <= GL_MOE_MAX_EXPERTS (64 when w1 or w2
- * is per group), top_k <= GL_MOE_MAX_TOP_K and <= E.  T == 0 does nothing.
+ * Limits: H % 8 == 0, F % 8 == 0, E <= GL_MOE_MAX_EXPERTS
+ * (GL_MOE_MAX_PER_GROUP when w1 or w2 is per group), top_k <= GL_MOE_MAX_TOP_K and <= E.  T == 0 does nothing.
  * Two launches, the second a cooperative one: it starts once every SM is free
  * for one of its blocks.
  */
 #define GL_MOE_MAX_TOKENS 128
 #define GL_MOE_MAX_EXPERTS 256
+#define GL_MOE_MAX_PER_GROUP 120
 #define GL_MOE_MAX_TOP_K 16
 #define GL_MOE_RENORM 1
 gl_status gl_moe_tokens(const void* x, const void* router, gl_grouped w1, gl_grouped w2, int act, int flags,

@@ -186,7 +186,7 @@ def test_nan_stays_with_its_token():
 
 
 def test_per_group_weights():
-    T, E, k, H, F = 10, 64, 4, 256, 128
+    T, E, k, H, F = 10, 120, 4, 256, 128
     x, router, w1, w2 = _layer(T, E, H, F)
     want = gl.gl_moe_tokens(x, w1, w2, k, _status(), router_w=router)[0]
     l1, l2 = [w1[e].clone() for e in range(E)], [w2[e].clone() for e in range(E)]

@@ -34,7 +34,7 @@ def test_invalid(kw):
 
 @pytest.mark.parametrize("kw", [
     dict(T=129), dict(E=257), dict(E=32, k=17), dict(H=60), dict(F=20), dict(x=8), dict(router=8), dict(y=8),
-    dict(ws=64), dict(idx=2), dict(w=2), dict(E=65, w1=_pg(65)), dict(E=65, w2=_pg(65)), dict(w1=_pg(8, 24))])
+    dict(ws=64), dict(idx=2), dict(w=2), dict(E=121, w1=_pg(121)), dict(E=121, w2=_pg(121)), dict(w1=_pg(8, 24))])
 def test_unsupported(kw):
     assert _m(**kw) == gl.GL_ERR_UNSUPPORTED
 

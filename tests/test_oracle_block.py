@@ -71,6 +71,22 @@ def test_activation_and_its_gradient_against_autograd(name):
 
 
 @pytest.mark.parametrize("name", blk.ACTS[1:])
+def test_activation_gradient_against_differences(name):
+    rng = np.random.default_rng(8)
+    z, w = rng.standard_normal((4, 12)) * 2, rng.standard_normal((1, 5, 12 // (2 if name in blk.GATED else 1)))
+    dy = rng.standard_normal((4, 5))
+
+    def loss(z):
+        return float(np.sum(blk.fwd_act(blk.act(name, z), w, None, [4], "none", None)[0] * dy))
+
+    dz, h = blk.dgrad_act(dy, w, [4], name, z), 1e-6
+    for i, j in ((0, 0), (1, 5), (2, 6), (3, 11)):
+        e = np.zeros_like(z)
+        e[i, j] = h
+        assert abs((loss(z + e) - loss(z - e)) / (2 * h) - dz[i, j]) < 1e-6 * (1 + abs(dz[i, j]))
+
+
+@pytest.mark.parametrize("name", blk.ACTS[1:])
 def test_grouped_products_with_activations_against_autograd(name):
     rng = np.random.default_rng(4)
     m = [5, 0, 3]
