@@ -426,14 +426,15 @@ def _refuse(what: str, why: str) -> None:
 
 def _tensor(what: str, name: str, t, dtype, shape) -> None:
     """Refuse anything but a contiguous tensor of this dtype and shape."""
-    if not isinstance(t, torch.Tensor):
-        _refuse(what, f"{name} must be a tensor")
-    if t.dtype is not dtype:
-        _refuse(what, f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        _refuse(what, f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
+    if isinstance(t, torch.Tensor):
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return
+        if t.dtype is not dtype:
+            _refuse(what, f"{name} must be {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            _refuse(what, f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
         _refuse(what, f"{name} must be contiguous")
+    _refuse(what, f"{name} must be a tensor")
 
 
 def _matrix(what: str, name: str, t) -> torch.Size:
@@ -450,28 +451,21 @@ def _status_word(what: str, t) -> None:
         _refuse(what, "status must be one int32")
 
 
-class _On:
-    """The device of a call's tensors, made current for the call; yields its current stream."""
+def _device(what: str, first: torch.Tensor, *others) -> int:
+    """The CUDA device that all of a call's tensors are on."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            _refuse(what, f"tensors on {first.device} and {t.device}")
+    if dev < 0:
+        _refuse(what, f"tensors must be on a CUDA device, not {first.device}")
+    return dev
 
-    __slots__ = ("dev", "old")
 
-    def __init__(self, what: str, first: torch.Tensor, *others):
-        self.dev = first.get_device()
-        for t in others:
-            if t is not None and t.get_device() != self.dev:
-                _refuse(what, f"tensors on {first.device} and {t.device}")
-        if self.dev < 0:
-            _refuse(what, f"tensors must be on a CUDA device, not {first.device}")
-
-    def __enter__(self) -> int:
-        self.old = torch.cuda.current_device()
-        if self.old != self.dev:
-            torch.cuda.set_device(self.dev)
-        return torch._C._cuda_getCurrentRawStream(self.dev)
-
-    def __exit__(self, *exc):
-        if self.old != self.dev:
-            torch.cuda.set_device(self.old)
+# the current device, and the handle of a device's current stream (what
+# torch.cuda.current_stream() wraps in an object; absent from a torch without CUDA)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def gl_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
@@ -497,41 +491,44 @@ def gl_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optio
     if mxfp8 and cols % (128 if mma_scales else 32):
         _refuse(what, f"cols = {cols} does not fit the scale layout")
     out = {} if out is None else dict(out)
-    with _On(what, x, gamma, residual, *out.values()) as stream:
-        rstd = out.get("rstd")
-        if rstd is None:
-            rstd = out["rstd"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+    dev = _device(what, x, gamma, residual, *out.values())
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return gl_rmsnorm(x, gamma, eps, residual, y, mxfp8, mma_scales, out)
+    rstd = out.get("rstd")
+    if rstd is None:
+        rstd = out["rstd"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        _tensor(what, "rstd", rstd, torch.float32, (rows,))
+    s = out.get("sum")
+    if s is not None:
+        _tensor(what, "sum", s, bf, shape)
+    elif residual is not None:
+        s = out["sum"] = torch.empty_like(x)
+    yt = out.get("y")
+    if yt is not None:
+        _tensor(what, "y", yt, bf, shape)
+    elif y:
+        yt = out["y"] = torch.empty_like(x)
+    codes, scales = out.get("codes_r"), out.get("scales_r")
+    if mxfp8:
+        if codes is None:
+            codes = out["codes_r"] = torch.empty_like(x, dtype=torch.uint8)
         else:
-            _tensor(what, "rstd", rstd, torch.float32, (rows,))
-        s = out.get("sum")
-        if s is not None:
-            _tensor(what, "sum", s, bf, shape)
-        elif residual is not None:
-            s = out["sum"] = torch.empty_like(x)
-        yt = out.get("y")
-        if yt is not None:
-            _tensor(what, "y", yt, bf, shape)
-        elif y:
-            yt = out["y"] = torch.empty_like(x)
-        codes, scales = out.get("codes_r"), out.get("scales_r")
-        if mxfp8:
-            if codes is None:
-                codes = out["codes_r"] = torch.empty_like(x, dtype=torch.uint8)
-            else:
-                _tensor(what, "codes_r", codes, torch.uint8, shape)
-            size = ((rows + 127) // 128 * (cols // 128) * 512,) if mma_scales else (rows, cols // 32)
-            if scales is None:
-                scales = out["scales_r"] = torch.empty(size, dtype=torch.uint8, device=x.device)
-            elif mma_scales:
-                _tensor(what, "scales_r", scales, torch.uint8, size)
-            else:  # [rows, cols / 32], or the same bytes in a row
-                _tensor(what, "scales_r", scales, torch.uint8, size if scales.dim() == 2 else (rows * (cols // 32),))
-        known = 1 + (s is not None) + y + 2 * mxfp8
-        if len(out) != known:
-            _refuse(what, f"out has {sorted(out)}: more than this call's outputs")
-        _check(load().gl_rmsnorm(x.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, rows, cols, _ptr(s), _ptr(yt),
-                                 rstd.data_ptr(), _ptr(codes), _ptr(scales),
-                                 GL_SCALES_MMA if mma_scales else GL_SCALES_ROWMAJOR, stream), what)
+            _tensor(what, "codes_r", codes, torch.uint8, shape)
+        size = ((rows + 127) // 128 * (cols // 128) * 512,) if mma_scales else (rows, cols // 32)
+        if scales is None:
+            scales = out["scales_r"] = torch.empty(size, dtype=torch.uint8, device=x.device)
+        elif mma_scales:
+            _tensor(what, "scales_r", scales, torch.uint8, size)
+        else:  # [rows, cols / 32], or the same bytes in a row
+            _tensor(what, "scales_r", scales, torch.uint8, size if scales.dim() == 2 else (rows * (cols // 32),))
+    known = 1 + (s is not None) + y + 2 * mxfp8
+    if len(out) != known:
+        _refuse(what, f"out has {sorted(out)}: more than this call's outputs")
+    _check(load().gl_rmsnorm(x.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, rows, cols, _ptr(s), _ptr(yt),
+                             rstd.data_ptr(), _ptr(codes), _ptr(scales),
+                             GL_SCALES_MMA if mma_scales else GL_SCALES_ROWMAJOR, _current_stream(dev)), what)
     return out
 
 
@@ -567,16 +564,20 @@ def gl_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, gamma: torch.Tensor, rst
         _tensor(what, "dgamma", dgamma, torch.float32, (cols,))
     if accumulate and dgamma is None:
         _refuse(what, "accumulate needs a dgamma")
-    with _On(what, dy, sum, gamma, rstd, dsum, dx, dgamma, workspace) as stream:
-        if dx is None:
-            dx = torch.empty_like(dy)
-        if dgamma is None:
-            dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
-        if workspace is None:
-            workspace = torch.empty(rmsnorm_bwd_workspace_bytes(rows, cols), dtype=torch.uint8, device=dy.device)
-        _check(load().gl_rmsnorm_bwd(dy.data_ptr(), sum.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), _ptr(dsum),
-                                     rows, cols, dx.data_ptr(), dgamma.data_ptr(), 1 if accumulate else 0,
-                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream), what)
+    dev = _device(what, dy, sum, gamma, rstd, dsum, dx, dgamma, workspace)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return gl_rmsnorm_bwd(dy, sum, gamma, rstd, dsum, dx, dgamma, accumulate, workspace)
+    if dx is None:
+        dx = torch.empty_like(dy)
+    if dgamma is None:
+        dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
+    if workspace is None:
+        workspace = torch.empty(rmsnorm_bwd_workspace_bytes(rows, cols), dtype=torch.uint8, device=dy.device)
+    _check(load().gl_rmsnorm_bwd(dy.data_ptr(), sum.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), _ptr(dsum),
+                                 rows, cols, dx.data_ptr(), dgamma.data_ptr(), 1 if accumulate else 0,
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 _current_stream(dev)), what)
     return dx, dgamma
 
 
@@ -642,19 +643,22 @@ def gl_fwd_act(x: torch.Tensor, w: TensorOrList, bias: Optional[TensorOrList], o
         _tensor(what, "z", z, torch.bfloat16, (M, N))
     if y is not None:
         _rows_at_least(what, "y", y, M, Nout)
-    with _On(what, x, w0, b0, residual, offsets, status, z, y) as stream:
-        if y is None:
-            y = torch.empty(M, Nout, dtype=torch.bfloat16, device=x.device)
-        if z is None and save_z:
-            z = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
-        wg, keep_w = _grouped(w, G)
-        bptr, keep_b = None, None
-        if bias is not None:
-            bg, keep_b = _grouped(bias, G)
-            bptr = ctypes.pointer(bg)
-        _check(load().gl_fwd_act(x.data_ptr(), wg, bptr, _ptr(residual), act, offsets.data_ptr(), status.data_ptr(),
-                                 G, M, N, K, _ptr(z), y.data_ptr(), y.shape[0], _opts_open(pair, wait_limit_us, opt_flags),
-                                 stream), what)
+    dev = _device(what, x, w0, b0, residual, offsets, status, z, y)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return gl_fwd_act(x, w, bias, offsets, status, act, residual, save_z, z, y, pair, wait_limit_us, opt_flags)
+    if y is None:
+        y = torch.empty(M, Nout, dtype=torch.bfloat16, device=x.device)
+    if z is None and save_z:
+        z = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+    wg, keep_w = _grouped(w, G)
+    bptr, keep_b = None, None
+    if bias is not None:
+        bg, keep_b = _grouped(bias, G)
+        bptr = ctypes.byref(bg)
+    _check(load().gl_fwd_act(x.data_ptr(), wg, bptr, _ptr(residual), act, offsets.data_ptr(), status.data_ptr(),
+                             G, M, N, K, _ptr(z), y.data_ptr(), y.shape[0], _opts_open(pair, wait_limit_us, opt_flags),
+                             _current_stream(dev)), what)
     del keep_w, keep_b
     return y, z
 
@@ -677,13 +681,16 @@ def gl_dgrad_act(dy: torch.Tensor, w: TensorOrList, z: torch.Tensor, offsets: to
     _tensor(what, "z", z, torch.bfloat16, (M, width))
     if dz is not None:
         _rows_at_least(what, "dz", dz, M, width)
-    with _On(what, dy, w0, z, offsets, status, dz) as stream:
-        if dz is None:
-            dz = torch.empty(M, width, dtype=torch.bfloat16, device=dy.device)
-        wg, keep = _grouped(w, G)
-        _check(load().gl_dgrad_act(dy.data_ptr(), wg, z.data_ptr(), act, offsets.data_ptr(), status.data_ptr(), G, M,
-                                   N, K, dz.data_ptr(), dz.shape[0], _opts_open(pair, wait_limit_us, opt_flags), stream),
-               what)
+    dev = _device(what, dy, w0, z, offsets, status, dz)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return gl_dgrad_act(dy, w, z, offsets, status, act, dz, pair, wait_limit_us, opt_flags)
+    if dz is None:
+        dz = torch.empty(M, width, dtype=torch.bfloat16, device=dy.device)
+    wg, keep = _grouped(w, G)
+    _check(load().gl_dgrad_act(dy.data_ptr(), wg, z.data_ptr(), act, offsets.data_ptr(), status.data_ptr(), G, M,
+                               N, K, dz.data_ptr(), dz.shape[0], _opts_open(pair, wait_limit_us, opt_flags), _current_stream(dev)),
+           what)
     del keep
     return dz
 
@@ -733,21 +740,25 @@ def gl_moe_tokens(x: torch.Tensor, w1: TensorOrList, w2: TensorOrList, top_k: in
         _tensor(what, "topk_w", topk_w, torch.float32, (T, top_k))
     if y is not None:
         _tensor(what, "y", y, bf, (T, H))
-    with _On(what, x, a, b, router_w, status, topk_idx, topk_w, y, workspace) as stream:
-        if topk_idx is None:
-            topk_idx = torch.empty(T, top_k, dtype=torch.int32, device=x.device)
-        if topk_w is None:
-            topk_w = torch.empty(T, top_k, dtype=torch.float32, device=x.device)
-        if y is None:
-            y = torch.empty_like(x)
-        if workspace is None:
-            workspace = torch.empty(moe_workspace_bytes(T, E, top_k, H, F), dtype=torch.uint8, device=x.device)
-        g1, keep1 = _grouped(w1, E)
-        g2, keep2 = _grouped(w2, E)
-        _check(load().gl_moe_tokens(x.data_ptr(), _ptr(router_w), g1, g2, act, GL_MOE_RENORM if renorm else 0, T, E,
-                                    top_k, H, F, topk_idx.data_ptr(), topk_w.data_ptr(), y.data_ptr(),
-                                    status.data_ptr(), workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), _opts(True, wait_limit_us, opt_flags),
-                                    stream), what)
+    dev = _device(what, x, a, b, router_w, status, topk_idx, topk_w, y, workspace)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return gl_moe_tokens(x, w1, w2, top_k, status, router_w, topk_idx, topk_w, act, renorm, y, workspace,
+                                 wait_limit_us, opt_flags)
+    if topk_idx is None:
+        topk_idx = torch.empty(T, top_k, dtype=torch.int32, device=x.device)
+    if topk_w is None:
+        topk_w = torch.empty(T, top_k, dtype=torch.float32, device=x.device)
+    if y is None:
+        y = torch.empty_like(x)
+    if workspace is None:
+        workspace = torch.empty(moe_workspace_bytes(T, E, top_k, H, F), dtype=torch.uint8, device=x.device)
+    g1, keep1 = _grouped(w1, E)
+    g2, keep2 = _grouped(w2, E)
+    _check(load().gl_moe_tokens(x.data_ptr(), _ptr(router_w), g1, g2, act, GL_MOE_RENORM if renorm else 0, T, E,
+                                top_k, H, F, topk_idx.data_ptr(), topk_w.data_ptr(), y.data_ptr(),
+                                status.data_ptr(), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _opts(True, wait_limit_us, opt_flags),
+                                _current_stream(dev)), what)
     del keep1, keep2
     return y, topk_idx, topk_w
