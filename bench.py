@@ -50,17 +50,17 @@ OP_SAMPLES = 50  # per-op medians are taken over at least this many steps
 # of the CUDA sources the capture ran.  When the sources have changed since,
 # the figures describe other kernels: the line then reports traffic as null.
 MEASURED_TRAFFIC = {
-    "csrc_digest": "f037632f4168708d",
+    "csrc_digest": "85a8bb45fc98d5cf",
     # the second step of `bench.py --steps 2 --warmup 3` under ncu (one pass,
     # gpu__time_duration / dram__bytes_read / dram__bytes_write per launch)
-    "bf16_g8": {"fwd": 1825746432, "dgrad": 2820858368, "wgrad": 5747676928,
-                "quant_x": 219182592, "quant_w": 1877729792, "quant_dy": 914067200,
-                "fwd_mx": 1006835200, "dgrad_mx": 1405178880, "wgrad_mx": 3657736704},
+    "bf16_g8": {"fwd": 1964868608, "dgrad": 3294173696, "wgrad": 5759185408,
+                "quant_x": 219350272, "quant_w": 1878397952, "quant_dy": 914446848,
+                "fwd_mx": 1011638016, "dgrad_mx": 1392854016, "wgrad_mx": 3667849728},
     # `bench.py --workload stacked_g128_ragged --steps 1 --warmup 1` under ncu
     # (the timed step's kernels; the MXFP8 wgrad from the warm-up step)
-    "stacked_g128_ragged": {"fwd": 5596950272, "dgrad": 4619833600, "wgrad": 15660184320,
-                            "quant_x": 1890677760, "quant_w": 7898937856, "quant_dy": 493870336,
-                            "fwd_mx": 2672948224, "dgrad_mx": 2815816448, "wgrad_mx": 14946737664},
+    "stacked_g128_ragged": {"fwd": 5554096128, "dgrad": 4617912064, "wgrad": 15630585856,
+                            "quant_x": 1890725376, "quant_w": 7900081152, "quant_dy": 493861120,
+                            "fwd_mx": 2663731712, "dgrad_mx": 2815709184, "wgrad_mx": 14916707072},
 }
 
 
