@@ -112,6 +112,47 @@ def test_gradient(m, K, N, name, pair):
     _check(dz[:M], ref, tol)
 
 
+@pytest.mark.parametrize("width", [8, 24, 136])
+@pytest.mark.parametrize("pair", [True, False])
+def test_rows_that_are_no_multiple_of_32_bytes(width, pair):
+    """Widths that are odd multiples of 8, and buffers that start 16 bytes past a 32-byte boundary."""
+    m, K = [70, 0, 3, 190], 40
+    M, G = sum(m), len(m)
+    x, w, b = _rand(M, K, seed=1), _rand(G, width, K, seed=2, std=0.3), _rand(G, width, seed=3)
+    r = _rand(M, width, seed=4)
+    off, st = offsets_on_device(m, M)
+    y, z = gl.gl_fwd_act(x, w, b, off, st, gl.GL_ACT_GELU, residual=r, save_z=True, pair=pair)
+    ref, u = blk.fwd_act(f64(x), f64(w), f64(b), m, "gelu", f64(r))
+    du = _sum_error(K, f64(x), f64(w), m) + 2.0 ** -23 * np.abs(u)
+    _check(z, u, du)
+    _check(y, ref, _value_error("gelu", u, du) + 2.0 ** -23 * np.abs(ref))
+    dy = _rand(M, K, seed=5)
+    w2 = _rand(G, K, width, seed=6, std=0.3)
+    for name, two in (("silu", 1), ("swiglu", 2), ("geglu", 2)):
+        zz = _rand(M, width * two, seed=7)
+        dz = gl.gl_dgrad_act(dy, w2, zz, off, st, gl.ACTS[name], pair=pair)
+        ref = blk.dgrad_act(f64(dy), f64(w2), m, name, f64(zz))
+        # |value|, |slope| and the other factor are below 6 here
+        ddh = (K / 16 + 16) * 2.0 ** -23 * orc.dgrad(np.abs(f64(dy)), np.abs(f64(w2)), m)
+        tol = 36 * (ddh + 2.0 ** -16 * (1 + np.abs(orc.dgrad(f64(dy), f64(w2), m))))
+        _check(dz, ref, np.concatenate([tol] * two, axis=1))
+    # the same bits through buffers off the 32-byte boundary
+    w16 = _rand(G, 32, K, seed=8, std=0.3)
+    want, wz = gl.gl_fwd_act(x, w16, None, off, st, gl.GL_ACT_SWIGLU, residual=_rand(M, 16, seed=9), save_z=True, pair=pair)
+
+    def shifted(rows, cols):
+        t = torch.zeros(rows * cols + 8, dtype=BF, device="cuda")[8:].view(rows, cols)
+        assert t.data_ptr() % 32 == 16
+        return t
+
+    res = shifted(M, 16)
+    res.copy_(_rand(M, 16, seed=9))
+    got, gz = gl.gl_fwd_act(x, w16, None, off, st, gl.GL_ACT_SWIGLU, residual=res, z=shifted(M, 32), y=shifted(M, 16),
+                            pair=pair)
+    assert torch.equal(got, want) and torch.equal(gz, wz)
+    assert int(st.item()) == 0
+
+
 @pytest.mark.parametrize("name", ["none", "relu", "relu2"])
 def test_integers_are_exact(name):
     m, K, N = [100, 0, 300, 7], 96, 264
