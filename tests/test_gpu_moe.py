@@ -292,3 +292,42 @@ def test_decoding_steps_of_two_blocks():
             _check_y(y, n, i, ww, w1, w2, "swiglu")
             stream = stream + blk.experts(norm, i, ww, f64(w1), f64(w2), "swiglu")
         assert orc.rel_frobenius(f64(out), stream) <= 1e-2
+
+
+def test_beside_other_kernels_on_other_streams():
+    """The cooperative kernel among products and norms of another stream and of another host thread."""
+    import threading
+
+    T, E, k, H, F = 5, 16, 4, 1024, 512
+    x, router, w1, w2 = _layer(T, E, H, F)
+    M, G = 4096, 8
+    a, w, gamma = _rand(M, H, seed=1), _rand(G, 2048, H, seed=2, std=0.03), _rand(H, seed=3, std=0.1) + 1
+    off, st = gl.gl_offsets(torch.full((G,), M // G, device="cuda"), M)
+    st2 = _status()
+    want = gl.gl_moe_tokens(x, w1, w2, k, st2, router_w=router)[0]
+    want_y = gl.gl_fwd_act(a, w, None, off, st, gl.GL_ACT_SWIGLU)[0]
+    want_n = gl.gl_rmsnorm(a, gamma, 1e-5)["y"]
+    torch.cuda.synchronize()
+    got, failed = {}, []
+
+    def work(name, f):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[name] = [f() for _ in range(20)]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # pragma: no cover
+            failed.append((name, e))
+
+    jobs = {"moe": lambda: gl.gl_moe_tokens(x, w1, w2, k, st2, router_w=router)[0],
+            "act": lambda: gl.gl_fwd_act(a, w, None, off, st, gl.GL_ACT_SWIGLU)[0],
+            "norm": lambda: gl.gl_rmsnorm(a, gamma, 1e-5)["y"]}
+    threads = [threading.Thread(target=work, args=j) for j in jobs.items()]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    assert int(st.item()) == 0 and int(st2.item()) == 0
+    assert all(torch.equal(v, want) for v in got["moe"])
+    assert all(torch.equal(v, want_y) for v in got["act"])
+    assert all(torch.equal(v, want_n) for v in got["norm"])
