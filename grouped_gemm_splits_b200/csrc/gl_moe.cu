@@ -584,8 +584,8 @@ __device__ __forceinline__ int atom_acq_rel_add1(int* p) {
   asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ void red_release_add1(int* p) {
-  asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+__device__ __forceinline__ void red_release_add(int* p, int n) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(n) : "memory");
 }
 // Orders generic-proxy accesses to global memory before later ones of the
 // async proxy (TMA) and the other way round.
@@ -848,7 +848,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       act_values(p.act, a);
       if (f < p.F) p.hbuf[static_cast<int64_t>(slot) * p.F + f] = __float2bfloat16_rn(a[0] * u1);
     };
+    // Finished tiles of expert ready_j that are not yet announced: other CTAs' TMA
+    // reads h, so the announcement takes a proxy fence and a release.  It is made
+    // once per expert: per tile it cost more than a tile's products where tokens are
+    // short (rows of 272 elements, 130 products a CTA: 264 us instead of 184).
+    int ready_j = 0, ready_n = 0;
+    auto announce = [&]() {
+      if (ready_n == 0) return;
+      fence_proxy_async_all();
+      bar_epilogue();
+      if (et == 0) red_release_add(&p.plan->ready[ready_j], ready_n);
+      ready_n = 0;
+    };
     const bool ok = for_segments(f1, cta, [&](const Segment& s) {
+      if (s.j != ready_j) announce();
+      ready_j = s.j;
       const int buf = it & 1;
       const uint32_t tph = (it >> 1) & 1;
       ++it;
@@ -901,23 +915,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_epilogue();
         if (!*flag) return true;
         const int r64 = et & 63;
-        for (int i = et >> 6; i < n; i += 2) {
-          float u0 = 0.0f, u1 = 0.0f;
+        constexpr int kSlots = 4;  // of every other slot, the partials asked for at once
+        for (int i0 = et >> 6; i0 < n; i0 += 2 * kSlots) {
+          float u0[kSlots] = {}, u1[kSlots] = {};
           for (int c = c0; c <= c1; ++c) {
             const int which = (c == c0 && s.first != f1.begin(c0)) ? 1 : 0;
-            const float* src = p.part1 + (static_cast<int64_t>(2 * c + which) * p.nt + i) * 128 + r64;
-            u0 += __ldcg(src);
-            u1 += __ldcg(src + 64);
+            const float* src = p.part1 + (static_cast<int64_t>(2 * c + which) * p.nt + i0) * 128 + r64;
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+              const int o = min(2 * i, n - 1 - i0) * 128;
+              u0[i] += __ldcg(src + o);
+              u1[i] += __ldcg(src + o + 64);
+            }
           }
-          store_h(off + i, f0 + r64, u0, u1);
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i)
+            if (i0 + 2 * i < n) store_h(off + i0 + 2 * i, f0 + r64, u0[i], u1[i]);
         }
       }
-      // h is read by other CTAs' TMA
-      fence_proxy_async_all();
-      bar_epilogue();
-      if (et == 0) red_release_add1(&p.plan->ready[s.j]);
+      ++ready_n;
       return true;
     });
+    if (ok) announce();
     if (ok)
       for_segments(f2, cta, [&](const Segment& s) {
         const int buf = it & 1;
@@ -985,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return c;
   };
-  if (tid == 0 && !*abort_flag) red_release_add1(&p.plan->grid_bar);
+  if (tid == 0 && !*abort_flag) red_release_add(&p.plan->grid_bar, 1);
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem_base, 256);
