@@ -126,16 +126,27 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the threads that share a row.  `part` is one of two buffers used in
-// turn, so one barrier per row is enough.
+// Sums over the threads that share a row, of N rows at once.  `part` is one of
+// two buffers used in turn, so one barrier per turn is enough.
+template <bool WARP_ROW, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[32]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+  if (WARP_ROW) return;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane == 0) part[i][threadIdx.x >> 5] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? part[i][lane] : 0.0f);
+}
+
 template <bool WARP_ROW>
 __device__ __forceinline__ float row_sum(float v, float* part) {
-  v = warp_sum(v);
-  if (WARP_ROW) return v;
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? part[lane] : 0.0f);
+  float a[1] = {v};
+  row_sums<WARP_ROW>(a, reinterpret_cast<float(*)[32]>(part));
+  return a[0];
 }
 
 struct NormParams {
@@ -167,18 +178,18 @@ struct Ring {
 
 // x, residual and the outputs may be the same buffers: a thread has read all
 // of its row's vectors before it writes any, and no other thread touches them.
-template <int VPT, bool WARP_ROW, bool MX, int DEPTH>
+template <int VPT, bool WARP_ROW, bool MX, bool RES, int ROWS, int DEPTH>
 __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
     rmsnorm_kernel(const NormParams p) {
   extern __shared__ __align__(16) uint8_t ring_s[];
-  __shared__ float part[2][32];
+  __shared__ float part[2][ROWS][32];
   const int tpr = WARP_ROW ? 32 : static_cast<int>(blockDim.x);
   const int t = WARP_ROW ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int rpb = WARP_ROW ? kWarpRowThreads / 32 : 1;
   const int nv = p.cols >> 3;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * rpb;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rpb + (WARP_ROW ? (threadIdx.x >> 5) : 0);
-  const Ring<VPT, 2, DEPTH> ring{smem_u32(ring_s) + threadIdx.x * 16, blockDim.x * 16};
+  const Ring<VPT, RES ? 2 : 1, DEPTH> ring{smem_u32(ring_s) + threadIdx.x * 16, blockDim.x * 16};
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
   const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(p.residual);
   auto fetch = [&](int64_t row, int slot) {
@@ -189,7 +200,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
         if (c < nv) {
           const int64_t at = row * p.cols + c * 8;
           cp_async16(ring.place(slot, 0, j), x + at);
-          if (res != nullptr) cp_async16(ring.place(slot, 1, j), res + at);
+          if (RES) cp_async16(ring.place(slot, 1, j), res + at);
         }
       }
     }
@@ -206,68 +217,80 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
   const float inv_n = 1.0f / static_cast<float>(p.cols);
   const int64_t atoms = (p.rows + 127) >> 7;  // MMA layout: atoms per k-group
   int slot = 0, buf = 0;
-  for (int64_t row = row0; row < p.rows; row += stride, buf ^= 1) {
-    const int64_t base = row * p.cols;
-    f2 v[VPT][4];
-    f2 ss = 0;
-    cp_async_wait<DEPTH - 1>();
+  for (int64_t turn = row0; turn < p.rows; turn += ROWS * stride, buf ^= 1) {
+    f2 v[ROWS][VPT][4];
+    float sum[ROWS];
+    cp_async_wait<DEPTH - ROWS>();
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (t + j * tpr < nv) {
-        const Words a = words(lds16(ring.place(slot, 0, j)));
+    for (int n = 0; n < ROWS; ++n) {  // behind the last row: what the place holds, for no output
+      f2 ss = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = f2_of_bf16(a.w[i]);
-        if (res != nullptr) {
-          const Words r = words(lds16(ring.place(slot, 1, j)));
+      for (int j = 0; j < VPT; ++j) {
+        if (t + j * tpr < nv) {
+          const Words a = words(lds16(ring.place(slot + n, 0, j)));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[j][i] = f2_add(v[j][i], f2_of_bf16(r.w[i]));
+          for (int i = 0; i < 4; ++i) v[n][j][i] = f2_of_bf16(a.w[i]);
+          if (RES) {
+            const Words r = words(lds16(ring.place(slot + n, 1, j)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[n][j][i] = f2_add(v[n][j][i], f2_of_bf16(r.w[i]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[n][j][i] = 0;
         }
-      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = 0;
+        for (int i = 0; i < 4; ++i) ss = f2_fma(v[n][j][i], v[n][j][i], ss);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ss = f2_fma(v[j][i], v[j][i], ss);
+      const float2 s2 = f2_get(ss);
+      sum[n] = s2.x + s2.y;
     }
-    const float2 s2 = f2_get(ss);
-    const float sum = row_sum<WARP_ROW>(s2.x + s2.y, part[buf]);
-    fetch(row + DEPTH * stride, slot);
-    slot = slot + 1 == DEPTH ? 0 : slot + 1;
-    const float rstd = 1.0f / sqrtf(fmaf(sum, inv_n, p.eps));
-    if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
-    const f2 rr = f2_make(rstd, rstd);
-    const int64_t srow = !MX ? 0 : p.mma_scales ? (row >> 7) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4
-                                                : row * (p.cols >> 5);
+    row_sums<WARP_ROW>(sum, part[buf]);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = t + j * tpr;
-      const bool in = c < nv;
-      if (in && p.sum != nullptr)
-        __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + base + c * 8), pack_vec(v[j]));
+    for (int n = 0; n < ROWS; ++n) fetch(turn + (DEPTH + n) * stride, slot + n);
+    slot = slot + ROWS == DEPTH ? 0 : slot + ROWS;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] = f2_mul(f2_mul(v[j][i], rr), f2_of_bf16(g[j].w[i]));
-      if (in && p.y != nullptr)
-        __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + base + c * 8), pack_vec(v[j]));
-      if (MX) {
-        float amax = 0.0f;
+    for (int n = 0; n < ROWS; ++n) {
+      const int64_t row = turn + n * stride;
+      if (n > 0 && row >= p.rows) break;
+      const int64_t base = row * p.cols;
+      const float rstd = 1.0f / sqrtf(fmaf(sum[n], inv_n, p.eps));
+      if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+      const f2 rr = f2_make(rstd, rstd);
+      const int64_t srow = !MX ? 0 : p.mma_scales ? (row >> 7) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4
+                                                  : row * (p.cols >> 5);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 u = f2_get(v[j][i]);
-          amax = fmaxf(amax, fmaxf(fabsf(u.x), fabsf(u.y)));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int e = e8m0_of(amax);
-        const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^-(e - 127)
-        const f2 ii = f2_make(inv, inv);
-        if (in) {
-          const uint2 q = make_uint2(e4m3x4(f2_mul(v[j][0], ii), f2_mul(v[j][1], ii)),
-                                     e4m3x4(f2_mul(v[j][2], ii), f2_mul(v[j][3], ii)));
-          __stcs(reinterpret_cast<uint2*>(p.codes + base + c * 8), q);
-          if ((c & 3) == 0) {
-            const int kb = c >> 2;
-            p.scales[srow + (p.mma_scales ? static_cast<int64_t>(kb >> 2) * atoms * 512 + (kb & 3) : kb)] =
-                static_cast<uint8_t>(e);
+      for (int j = 0; j < VPT; ++j) {
+        const int c = t + j * tpr;
+        const bool in = c < nv;
+        f2(&u)[4] = v[n][j];
+        if (in && p.sum != nullptr)
+          __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + base + c * 8), pack_vec(u));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = f2_mul(f2_mul(u[i], rr), f2_of_bf16(g[j].w[i]));
+        if (in && p.y != nullptr)
+          __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + base + c * 8), pack_vec(u));
+        if (MX) {
+          float amax = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 w = f2_get(u[i]);
+            amax = fmaxf(amax, fmaxf(fabsf(w.x), fabsf(w.y)));
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          const int e = e8m0_of(amax);
+          const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^-(e - 127)
+          const f2 ii = f2_make(inv, inv);
+          if (in) {
+            const uint2 q = make_uint2(e4m3x4(f2_mul(u[0], ii), f2_mul(u[1], ii)),
+                                       e4m3x4(f2_mul(u[2], ii), f2_mul(u[3], ii)));
+            __stcs(reinterpret_cast<uint2*>(p.codes + base + c * 8), q);
+            if ((c & 3) == 0) {
+              const int kb = c >> 2;
+              p.scales[srow + (p.mma_scales ? static_cast<int64_t>(kb >> 2) * atoms * 512 + (kb & 3) : kb)] =
+                  static_cast<uint8_t>(e);
+            }
           }
         }
       }
@@ -462,21 +485,24 @@ int blocks_for(const NormPlan& pl, int64_t rows, bool backward) {
   return static_cast<int>(std::min<int64_t>(need, static_cast<int64_t>(num_sms()) * per_sm(pl, backward)));
 }
 
-template <int VPT, bool WARP_ROW, bool MX, int DEPTH>
+template <int VPT, bool WARP_ROW, bool MX, bool RES, int ROWS, int DEPTH>
 gl_status run_fwd(const NormPlan& pl, int grid, const NormParams& p, cudaStream_t s) {
-  auto kern = rmsnorm_kernel<VPT, WARP_ROW, MX, DEPTH>;
-  const int smem = Ring<VPT, 2, DEPTH>::bytes(pl.threads);
+  auto kern = rmsnorm_kernel<VPT, WARP_ROW, MX, RES, ROWS, DEPTH>;
+  const int smem = Ring<VPT, RES ? 2 : 1, DEPTH>::bytes(pl.threads);
   if (set_max_smem(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return GL_ERR_CUDA;
   kern<<<grid, pl.threads, smem, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? GL_OK : GL_ERR_CUDA;
 }
 
-// Two rows in flight per block, three where an SM holds one block only.
-template <bool MX>
+// Two rows in flight per block, three where an SM holds one block only; without
+// a residual twice that, for the same bytes, and two rows a turn.
+template <bool MX, bool RES>
 gl_status launch_fwd(const NormPlan& pl, int grid, const NormParams& p, cudaStream_t s) {
-  if (pl.warp_row) return run_fwd<1, true, MX, 2>(pl, grid, p, s);
-  if (pl.vpt == 2) return run_fwd<2, false, MX, 3>(pl, grid, p, s);
-  return per_sm(pl, false) > 1 ? run_fwd<1, false, MX, 2>(pl, grid, p, s) : run_fwd<1, false, MX, 3>(pl, grid, p, s);
+  constexpr int R = RES ? 1 : 2;
+  if (pl.warp_row) return run_fwd<1, true, MX, RES, R, 2 * R>(pl, grid, p, s);
+  if (pl.vpt == 2) return run_fwd<2, false, MX, RES, 1, 3 * R>(pl, grid, p, s);
+  return per_sm(pl, false) > 1 ? run_fwd<1, false, MX, RES, R, 2 * R>(pl, grid, p, s)
+                               : run_fwd<1, false, MX, RES, R, 3 * R>(pl, grid, p, s);
 }
 
 template <int VPT, bool WARP_ROW>
@@ -497,7 +523,9 @@ gl_status launch_rmsnorm(const void* x, const void* residual, const void* gamma,
   const NormPlan pl = plan_for(cols);
   NormParams p{x, residual, gamma, eps, rows, cols, sum, y, rstd, codes, scales, scale_layout == GL_SCALES_MMA};
   const int grid = blocks_for(pl, rows, false);
-  return codes != nullptr ? launch_fwd<true>(pl, grid, p, stream) : launch_fwd<false>(pl, grid, p, stream);
+  if (residual != nullptr)
+    return codes != nullptr ? launch_fwd<true, true>(pl, grid, p, stream) : launch_fwd<false, true>(pl, grid, p, stream);
+  return codes != nullptr ? launch_fwd<true, false>(pl, grid, p, stream) : launch_fwd<false, false>(pl, grid, p, stream);
 }
 
 int64_t rmsnorm_bwd_blocks(int64_t rows, int cols) { return blocks_for(plan_for(cols), rows, true); }
