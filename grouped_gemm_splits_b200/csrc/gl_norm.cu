@@ -27,6 +27,10 @@
 // and writes meet in DRAM: 32768 x 4096 to MXFP8 took 147 us with two blocks of
 // 512 and two rows each in flight, 155 us with three rows, 179 us with four
 // blocks of 256 (two vectors a thread) and three rows; the floor is 144 us.
+// Without a residual the same threads have one tensor to load, and a row's two
+// reductions are what they wait for: two rows a turn share them, and the ring
+// holds twice the rows (16384 x 7168 to bf16: 74 us, with one row a turn 98, with
+// the shorter ring 103; floor 72.  To MXFP8 90 us of 54: 76% of the issue slots are taken).
 // Measured with it: 65536 x 7168 to MXFP8 511 us (floor 504), to bf16 571
 // (574); 32768 x 2048 81 (72) and 88 (82); backward 32768 x 4096 164 (164).
 #include <cuda_bf16.h>
@@ -126,6 +130,13 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// 1 / sqrt(a): rsqrtf and one Newton step, a dozen instructions fewer in every
+// thread than a square root and a division.  Zero and infinity stay rsqrtf's.
+__device__ __forceinline__ float inv_sqrt(float a) {
+  const float r = rsqrtf(a), e = fmaf(-a * r, r, 1.0f);
+  return fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
+}
+
 // Sums over the threads that share a row, of N rows at once.  `part` is one of
 // two buffers used in turn, so one barrier per turn is enough.
 template <bool WARP_ROW, int N>
@@ -208,11 +219,13 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
   };
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i) fetch(row0 + i * stride, i);
-  Words g[VPT];
+  f2 g[VPT][4];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int c = t + j * tpr;
-    g[j] = words(c < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma) + c) : make_uint4(0, 0, 0, 0));
+    const Words w = words(c < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma) + c) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[j][i] = f2_of_bf16(w.w[i]);
   }
   const float inv_n = 1.0f / static_cast<float>(p.cols);
   const int64_t atoms = (p.rows + 127) >> 7;  // MMA layout: atoms per k-group
@@ -254,7 +267,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
       const int64_t row = turn + n * stride;
       if (n > 0 && row >= p.rows) break;
       const int64_t base = row * p.cols;
-      const float rstd = 1.0f / sqrtf(fmaf(sum[n], inv_n, p.eps));
+      const float rstd = inv_sqrt(fmaf(sum[n], inv_n, p.eps));
       if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
       const f2 rr = f2_make(rstd, rstd);
       const int64_t srow = !MX ? 0 : p.mma_scales ? (row >> 7) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4
@@ -267,7 +280,7 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowThreads : kMaxThreads)
         if (in && p.sum != nullptr)
           __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + base + c * 8), pack_vec(u));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = f2_mul(f2_mul(u[i], rr), f2_of_bf16(g[j].w[i]));
+        for (int i = 0; i < 4; ++i) u[i] = f2_mul(f2_mul(u[i], rr), g[j][i]);
         if (in && p.y != nullptr)
           __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + base + c * 8), pack_vec(u));
         if (MX) {
@@ -495,12 +508,13 @@ gl_status run_fwd(const NormPlan& pl, int grid, const NormParams& p, cudaStream_
 }
 
 // Two rows in flight per block, three where an SM holds one block only; without
-// a residual twice that, for the same bytes, and two rows a turn.
+// a residual twice that, for the same bytes, and two rows a turn (rows of two
+// vectors a thread stay at three: 8192 x 12288 took 68 us with them, 73 with six).
 template <bool MX, bool RES>
 gl_status launch_fwd(const NormPlan& pl, int grid, const NormParams& p, cudaStream_t s) {
   constexpr int R = RES ? 1 : 2;
   if (pl.warp_row) return run_fwd<1, true, MX, RES, R, 2 * R>(pl, grid, p, s);
-  if (pl.vpt == 2) return run_fwd<2, false, MX, RES, 1, 3 * R>(pl, grid, p, s);
+  if (pl.vpt == 2) return run_fwd<2, false, MX, RES, 1, 3>(pl, grid, p, s);
   return per_sm(pl, false) > 1 ? run_fwd<1, false, MX, RES, R, 2 * R>(pl, grid, p, s)
                                : run_fwd<1, false, MX, RES, R, 3 * R>(pl, grid, p, s);
 }

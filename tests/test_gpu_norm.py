@@ -87,6 +87,40 @@ def test_forward_mxfp8(rows, cols, mma, with_y):
     assert flat[0] == 127 and not (out["codes_r"][0, :32] & 0x7F).any()
 
 
+# Without a residual a block takes rows two at a time, `grid` rows apart: row
+# counts that end in the first or the second of them, and before the ring fills.
+@pytest.mark.parametrize("rows,cols", [(1, 128), (2, 1024), (149, 4096), (297, 4096), (1037, 2048), (1776, 2048),
+                                       (5000, 256), (4, 7168), (593, 7168), (741, 16384)])
+def test_forward_without_residual(rows, cols):
+    x, gamma = _rand(rows, cols, seed=rows), _rand(cols, seed=cols, std=0.5, mean=1.0)
+    out = gl.gl_rmsnorm(x, gamma, EPS, mxfp8=True, mma_scales=True)
+    _, rstd, y = blk.rmsnorm(f64(x), None, f64(gamma), EPS)
+    assert np.all(np.abs(f64(out["rstd"]) - rstd) <= F32 * rstd)
+    _close_bf16(out["y"], y)
+    _check_codes(out["codes_r"], out["scales_r"], y, True)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_mean_squares_at_the_ends_of_fp32(residual):
+    cols = 512
+    x = torch.ones(6, cols, dtype=BF, device="cuda")
+    x[0] = 2.0 ** 100  # the squares overflow: rstd is 0
+    x[1] = 2.0 ** -100  # and vanish: eps decides
+    x[2] = 2.0 ** 62  # their sum overflows: 512 * 2^124 = 2^133
+    x[3] = 2.0 ** -62
+    x[4] = 0.0
+    gamma = torch.ones(cols, dtype=BF, device="cuda")
+    r = torch.zeros_like(x) if residual else None
+    for eps in (1e-5, 1e-38):
+        out = gl.gl_rmsnorm(x, gamma, eps, residual=r)
+        _, rstd, y = blk.rmsnorm(f64(x), None, f64(gamma), eps)
+        over = (f64(x) ** 2).sum(1) >= 2.0 ** 128
+        assert list(over) == [True, False, True, False, False, False]
+        rstd[over], y[over] = 0, 0
+        assert np.all(np.abs(f64(out["rstd"]) - rstd) <= F32 * rstd)
+        _close_bf16(out["y"], y)
+
+
 def test_bytes_of_absent_rows_and_outputs_not_asked_for_stay():
     rows, cols = 5, 256
     x, gamma = _rand(rows, cols), _rand(cols, mean=1.0)
