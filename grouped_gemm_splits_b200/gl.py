@@ -455,11 +455,20 @@ def _device(what: str, first: torch.Tensor, *others) -> int:
     """The CUDA device that all of a call's tensors are on."""
     dev = first.get_device()
     for t in others:
-        if t is not None and t.get_device() != dev:
-            _refuse(what, f"tensors on {first.device} and {t.device}")
+        if t is not None:
+            if not isinstance(t, torch.Tensor):
+                _refuse(what, f"{t!r} is not a tensor")
+            if t.get_device() != dev:
+                _refuse(what, f"tensors on {first.device} and {t.device}")
     if dev < 0:
         _refuse(what, f"tensors must be on a CUDA device, not {first.device}")
     return dev
+
+
+def _scratch(what: str, t) -> None:
+    """Refuse a workspace whose elements are not all there in a row."""
+    if not isinstance(t, torch.Tensor) or not t.is_contiguous():
+        _refuse(what, "workspace must be a contiguous tensor")
 
 
 # the current device, and the handle of a device's current stream (what
@@ -564,6 +573,8 @@ def gl_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, gamma: torch.Tensor, rst
         _tensor(what, "dgamma", dgamma, torch.float32, (cols,))
     if accumulate and dgamma is None:
         _refuse(what, "accumulate needs a dgamma")
+    if workspace is not None:
+        _scratch(what, workspace)
     dev = _device(what, dy, sum, gamma, rstd, dsum, dx, dgamma, workspace)
     if dev != _current_device():
         with torch.cuda.device(dev):
@@ -585,6 +596,14 @@ def gl_rmsnorm_bwd(dy: torch.Tensor, sum: torch.Tensor, gamma: torch.Tensor, rst
 
 def _gated(act: int) -> bool:
     return act in (GL_ACT_SWIGLU, GL_ACT_GEGLU)
+
+
+def _weight_dims(what: str, name: str, w: TensorOrList):
+    """Rows and columns of a group's weight."""
+    t = w if isinstance(w, torch.Tensor) else w[0] if len(w) else None
+    if not isinstance(t, torch.Tensor) or t.dim() < 2:
+        _refuse(what, f"{name} must be a [groups, rows, cols] tensor or a list of matrices")
+    return t.shape[-2], t.shape[-1]
 
 
 def _weights(what: str, name: str, w: TensorOrList, G: int, shape) -> torch.Tensor:
@@ -631,7 +650,7 @@ def gl_fwd_act(x: torch.Tensor, w: TensorOrList, bias: Optional[TensorOrList], o
     M, K = _matrix(what, "x", x)
     if not GL_ACT_NONE <= act <= GL_ACT_GEGLU:
         _refuse(what, f"unknown activation {act}")
-    N = _shape_nk(w)[0]
+    N = _weight_dims(what, "w", w)[0]
     if _gated(act) and N % 2:
         _refuse(what, f"a gated activation halves {N} columns")
     w0 = _weights(what, "w", w, G, (N, K))
@@ -675,7 +694,7 @@ def gl_dgrad_act(dy: torch.Tensor, w: TensorOrList, z: torch.Tensor, offsets: to
     M, N = _matrix(what, "dy", dy)
     if not GL_ACT_NONE < act <= GL_ACT_GEGLU:
         _refuse(what, f"activation {act} has no slope to apply")
-    K = _shape_nk(w)[1]
+    K = _weight_dims(what, "w", w)[1]
     w0 = _weights(what, "w", w, G, (N, K))
     width = 2 * K if _gated(act) else K
     _tensor(what, "z", z, torch.bfloat16, (M, width))
@@ -724,8 +743,8 @@ def gl_moe_tokens(x: torch.Tensor, w1: TensorOrList, w2: TensorOrList, top_k: in
     bf = torch.bfloat16
     T, H = _matrix(what, "x", x)
     _status_word(what, status)
-    E = len(w1)
-    F = _shape_nk(w2)[1]
+    _weight_dims(what, "w1", w1)
+    E, F = len(w1), _weight_dims(what, "w2", w2)[1]
     a = _weights(what, "w1", w1, E, (2 * F, H))
     b = _weights(what, "w2", w2, E, (H, F))
     if T > GL_MOE_MAX_TOKENS:
@@ -740,6 +759,8 @@ def gl_moe_tokens(x: torch.Tensor, w1: TensorOrList, w2: TensorOrList, top_k: in
         _tensor(what, "topk_w", topk_w, torch.float32, (T, top_k))
     if y is not None:
         _tensor(what, "y", y, bf, (T, H))
+    if workspace is not None:
+        _scratch(what, workspace)
     dev = _device(what, x, a, b, router_w, status, topk_idx, topk_w, y, workspace)
     if dev != _current_device():
         with torch.cuda.device(dev):

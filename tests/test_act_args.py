@@ -73,3 +73,11 @@ OFF, ST = torch.zeros(3, dtype=torch.int64), torch.zeros(1, dtype=torch.int32)
 def test_binding_refuses(make):
     with pytest.raises(gl.GlError):
         make()
+
+
+@pytest.mark.parametrize("w", [[], _z(16), [None, None]])
+def test_binding_names_the_weight_it_refuses(w):
+    with pytest.raises(gl.GlError, match="w must be"):
+        gl.gl_fwd_act(_z(4, 16), w, None, OFF, ST, gl.GL_ACT_SILU)
+    with pytest.raises(gl.GlError, match="w must be"):
+        gl.gl_dgrad_act(_z(4, 32), w, _z(4, 16), OFF, ST, gl.GL_ACT_SILU)

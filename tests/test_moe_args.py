@@ -87,3 +87,15 @@ ST = torch.zeros(1, dtype=torch.int32)
 def test_binding_refuses(make):
     with pytest.raises(gl.GlError):
         make()
+
+
+@pytest.mark.parametrize("w1,w2,ws,why", [
+    ([], [], None, "w1 must be"),
+    (torch.tensor(0.0), _z(4, 64, 16), None, "w1 must be"),
+    (_z(4, 32, 64), [], None, "w2 must be"),
+    (_z(4, 32, 64), _z(16), None, "w2 must be"),
+    (_z(4, 32, 64), _z(4, 64, 16), torch.zeros(1, dtype=torch.uint8).expand(1 << 24), "workspace must be"),
+])
+def test_binding_names_what_it_refuses(w1, w2, ws, why):
+    with pytest.raises(gl.GlError, match=why):
+        gl.gl_moe_tokens(_z(2, 64), w1, w2, 2, ST, router_w=_z(4, 64), workspace=ws)

@@ -76,3 +76,13 @@ def _z(*shape, dtype=BF):
 def test_binding_refuses(make):
     with pytest.raises(gl.GlError):
         make()
+
+
+def test_binding_names_what_it_refuses():
+    rstd = _z(4, dtype=torch.float32)
+    with pytest.raises(gl.GlError, match="workspace must be"):  # one byte, many times
+        gl.gl_rmsnorm_bwd(_z(4, 64), _z(4, 64), _z(64), rstd, workspace=_z(1, dtype=U8).expand(1 << 20))
+    with pytest.raises(gl.GlError, match="workspace must be"):
+        gl.gl_rmsnorm_bwd(_z(4, 64), _z(4, 64), _z(64), rstd, workspace=1 << 20)
+    with pytest.raises(gl.GlError, match="not a tensor"):
+        gl.gl_rmsnorm(_z(4, 64), _z(64), 1e-5, out={"y": [0.0]})
