@@ -50,17 +50,17 @@ OP_SAMPLES = 50  # per-op medians are taken over at least this many steps
 # of the CUDA sources the capture ran.  When the sources have changed since,
 # the figures describe other kernels: the line then reports traffic as null.
 MEASURED_TRAFFIC = {
-    "csrc_digest": "85a8bb45fc98d5cf",
+    "csrc_digest": "05899e12ae36d1bb",
     # the second step of `bench.py --steps 2 --warmup 3` under ncu (one pass,
     # gpu__time_duration / dram__bytes_read / dram__bytes_write per launch)
-    "bf16_g8": {"fwd": 1964868608, "dgrad": 3294173696, "wgrad": 5759185408,
-                "quant_x": 219350272, "quant_w": 1878397952, "quant_dy": 914446848,
-                "fwd_mx": 1011638016, "dgrad_mx": 1392854016, "wgrad_mx": 3667849728},
+    "bf16_g8": {"fwd": 1962336512, "dgrad": 3284737792, "wgrad": 5773288704,
+                "quant_x": 219350528, "quant_w": 1878191104, "quant_dy": 914407680,
+                "fwd_mx": 1007970816, "dgrad_mx": 1400205312, "wgrad_mx": 3673631232},
     # `bench.py --workload stacked_g128_ragged --steps 1 --warmup 1` under ncu
     # (the timed step's kernels; the MXFP8 wgrad from the warm-up step)
-    "stacked_g128_ragged": {"fwd": 5554096128, "dgrad": 4617912064, "wgrad": 15630585856,
-                            "quant_x": 1890725376, "quant_w": 7900081152, "quant_dy": 493861120,
-                            "fwd_mx": 2663731712, "dgrad_mx": 2815709184, "wgrad_mx": 14916707072},
+    "stacked_g128_ragged": {"fwd": 6857675008, "dgrad": 4629791488, "wgrad": 15535091456,
+                            "quant_x": 1891062784, "quant_w": 7906281216, "quant_dy": 493842944,
+                            "fwd_mx": 2874321152, "dgrad_mx": 2815959040, "wgrad_mx": 14829575680},
 }
 
 

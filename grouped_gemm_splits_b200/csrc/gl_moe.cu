@@ -35,7 +35,7 @@
 //
 // Measured (time of both launches against the weights' bytes at the copy
 // bandwidth): 13 tokens, top 8 of 128 experts of 7168 x 2048 970-993 us (978);
-// 64 tokens, top 6 of 64 experts of 2048 x 1408 188-197 us (169); one token, top
+// 64 tokens, top 6 of 64 experts of 2048 x 1408 187-196 us (169); one token, top
 // 2 of 8 experts of 4096 x 14336 120-122 us (108); one token, top 6 of 64 of
 // 2048 x 1408 37 us (16).  The last is a chain of latencies: routing 6.6 us, 3 us
 // to the second kernel, its set-up and first weights 3.9, W1 10.5, h to the
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Finished tiles of expert ready_j that are not yet announced: other CTAs' TMA
     // reads h, so the announcement takes a proxy fence and a release.  It is made
     // once per expert: per tile it cost more than a tile's products where tokens are
-    // short (rows of 272 elements, 130 products a CTA: 264 us instead of 184).
+    // short (20 tokens, top 4 of 129 experts of 272 x 8312: 263 us instead of 190).
     int ready_j = 0, ready_n = 0;
     auto announce = [&]() {
       if (ready_n == 0) return;
