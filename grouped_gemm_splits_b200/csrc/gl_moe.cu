@@ -993,7 +993,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile = item % tiles, t = item / tiles * tpi + warp / wpt;
     if (item < items && t < p.T && lane < p.k) {
       c.pos = p.plan->pos_of[t * p.k + lane];
-      c.w = p.w[t * p.k + lane];
+      const float w = p.w[t * p.k + lane];
+      c.w = c.pos >= 0 ? w : 0.0f;  // an absent choice's weight may be anything: 0 times a NaN is one
       if (c.pos >= 0) {
         const int j = p.plan->slot_act[c.pos];
         const int64_t first = (static_cast<int64_t>(j) * tiles + tile) * f2.kb;

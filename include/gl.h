@@ -531,8 +531,9 @@ size_t gl_rmsnorm_bwd_workspace_bytes(int64_t rows, int cols);
  *   x         device bf16 [T, H]
  *   router    device bf16 [E, H], or NULL: topk_idx and topk_w are then
  *             inputs (a caller's own routing; any weights).  An index of -1
- *             is no expert: such a choice adds nothing, and a token without
- *             any gets zeros (the padding of a captured batch).
+ *             is no expert: such a choice adds nothing, whatever its weight
+ *             (NaN or infinite too), and a token without any gets zeros
+ *             (the padding of a captured batch).
  *   w1        bf16 [E, 2F, H] stacked or E pointers to [2F, H] (the F rows of
  *             the activated factor first, as for gl_fwd_act)
  *   w2        bf16 [E, H, F] stacked or E pointers to [H, F]

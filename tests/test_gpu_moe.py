@@ -331,3 +331,27 @@ def test_beside_other_kernels_on_other_streams():
     assert all(torch.equal(v, want) for v in got["moe"])
     assert all(torch.equal(v, want_y) for v in got["act"])
     assert all(torch.equal(v, want_n) for v in got["norm"])
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 9, 128])
+def test_weights_of_absent_choices_are_not_used(T):
+    """NaN and infinite weights at index -1: the bits that zeros there give, and zeros for a token without experts."""
+    E, k, H, F = 12, 4, 192, 104
+    x, _, w1, w2 = _layer(T, E, H, F, seed=T)
+    rng = np.random.default_rng(T)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    idx[rng.random((T, k)) < 0.4] = -1
+    idx[0] = [-1, 3, -1, 7]  # every token count has a token that drops some of its choices
+    if T > 1:
+        idx[1] = -1
+    w = rng.standard_normal((T, k)).astype(np.float32)
+    ti = torch.tensor(idx).cuda()
+    want = gl.gl_moe_tokens(x, w1, w2, k, _status(), topk_idx=ti, topk_w=torch.tensor(np.where(idx < 0, 0, w)).cuda())[0]
+    _check_y(want, x, idx, w.astype(np.float64), w1, w2, "swiglu")
+    for v in (np.nan, np.inf, -np.inf):
+        st = _status()
+        tw = torch.tensor(np.where(idx < 0, np.float32(v), w)).cuda()
+        y = gl.gl_moe_tokens(x, w1, w2, k, st, topk_idx=ti, topk_w=tw)[0]
+        assert torch.equal(y, want) and int(st.item()) == 0
+        if T > 1:
+            assert not y[1].any()
