@@ -64,7 +64,8 @@ constexpr int kPG = GL_MOE_MAX_PER_GROUP;  // experts whose tensor maps a launch
 struct Plan {
   int grid_bar;
   int n_act;             // experts that some token reaches
-  int pad[62];
+  int skip;              // the status word was set, or the routing is bad: nothing is written
+  int pad[61];
   int ready[kMaxE];      // finished h tiles of each active expert
   int cut[kMaxCtas];     // arrivals at the W1 tile that starts in CTA c and ends in a later one
   int act_e[kMaxE];      // active experts, ascending
@@ -124,6 +125,10 @@ __device__ __forceinline__ float route_sum(float v) {
 __device__ __forceinline__ void st_cluster_u16(uint32_t addr, uint16_t v) {
   asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -199,14 +204,16 @@ __device__ __forceinline__ void route_logits(const RouteParams& p, const RouteSp
 // One warp picks token t's experts, from the sums of all CTAs' parts, and
 // leaves them in the first CTA's s_idx too.  Keys order by value, equal ones
 // by the lower index; a NaN orders last but stays a candidate, so that k valid
-// experts always come out (and the token's weights become NaN).
-__device__ __forceinline__ void route_pick(const RouteParams& p, const float* part, const short* s_idx, int t,
-                                           int lane, bool skip) {
+// experts always come out (and the token's weights become NaN).  Of s_skip the
+// first CTA's counts.
+__device__ __forceinline__ void route_pick(const RouteParams& p, const float* part, const short* s_idx,
+                                           const int* s_skip, int t, int lane) {
   constexpr int kPer = kMaxE / 32;
   const int per = (p.E + 31) >> 5;
   float v[kPer];
   uint32_t key[kPer];
   float m = __int_as_float(0xff800000);
+  const bool skip = __float_as_int(ld_cluster_f32(mapa_shared(smem_u32(s_skip), 0))) != 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + i * 32;
@@ -271,13 +278,17 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __maxnreg__(80)
     route_kernel(const RouteParams p) {
   extern __shared__ float part[];  // logits over this CTA's part of H; then the first CTA's histograms
   __shared__ short s_idx[kMaxSlots];
-  __shared__ int s_cnt[kMaxE + 1], s_act[kMaxE + 1], s_bad;
+  __shared__ int s_cnt[kMaxE + 1], s_act[kMaxE + 1], s_bad, s_skip;
   const int rank = static_cast<int>(cluster_ctarank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_launch_dependents();  // experts_kernel may set itself up meanwhile
-  // A set status word only holds back the outputs: a CTA that left early would
-  // take its shared memory from the others.
-  const bool skip = *reinterpret_cast<volatile int32_t*>(p.status) != 0;
+  // The status word is read once, by one thread: a call beside this one may set it
+  // meanwhile, and where threads or CTAs went by different values, some would wait
+  // at barriers for others that had left.  A set word only holds back the outputs:
+  // here s_skip (the word itself, copied while the logits are formed), in the next
+  // kernel the plan's copy.
+  const bool reader = rank == 0 && tid == 0;
+  if (reader) cp_async4(smem_u32(&s_skip), p.status);
   Plan* pl = p.plan;
   const int S = p.T * p.k;
   const bool few = p.T <= kRouteWarps;  // the first CTA picks for all tokens
@@ -300,14 +311,16 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __maxnreg__(80)
         part[i] = v;
       }
     }
+    if (reader) cp_async_wait_all();
     cluster_sync();
     if (few) {
-      if (rank == 0 && warp < p.T) route_pick(p, part, s_idx, warp, lane, skip);
+      if (rank == 0 && warp < p.T) route_pick(p, part, s_idx, &s_skip, warp, lane);
     } else {
       for (int t = rank + kRouteCtas * warp; t < p.T; t += kRouteCtas * kRouteWarps)
-        route_pick(p, part, s_idx, t, lane, skip);
+        route_pick(p, part, s_idx, &s_skip, t, lane);
     }
   } else if (rank == 0) {
+    if (reader) cp_async_wait_all();
     for (int s = tid; s < S; s += kRouteThreads) {
       const int e = p.idx[s];
       const bool ok = e >= -1 && e < p.E;
@@ -358,6 +371,7 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __maxnreg__(80)
       if (lane == 0) {
         pl->n_act = n_act;
         pl->act_off[n_act] = n;
+        pl->skip = s_skip | s_bad;
         if (s_bad) atomicOr(p.status, GL_DEV_BAD_INDEX);
       }
     }
@@ -443,6 +457,7 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __maxnreg__(80)
   if (tid == 0) {
     pl->n_act = s_act[kMaxE];
     pl->act_off[s_act[kMaxE]] = s_cnt[kMaxE];
+    pl->skip = s_skip | s_bad;
     if (s_bad) atomicOr(p.status, GL_DEV_BAD_INDEX);
   }
   if (few) cluster_wait();
@@ -672,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dependency_wait();  // route_kernel's results from here on
   // the plan: all of it at once, whatever part is in use, so that its loads overlap
-  const int status = *reinterpret_cast<volatile int32_t*>(p.status);
+  const int skip = p.plan->skip;  // one value for the whole grid: its CTAs and warps wait for one another
   const int n_act = p.plan->n_act;
   static_assert(kThreads == kMaxE, "one expert a thread");
   act_e[tid] = p.plan->act_e[tid];
@@ -683,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  if (status != 0) {
+  if (skip != 0) {
     if (warp == 2) tmem_dealloc(tmem_base, 256);
     return;
   }

@@ -542,8 +542,8 @@ size_t gl_rmsnorm_bwd_workspace_bytes(int64_t rows, int cols);
  *   topk_idx  device int32 [T, top_k], written (read when router is NULL)
  *   topk_w    device fp32 [T, top_k], likewise
  *   y         device bf16 [T, H], written
- *   status    device int32 status word (required): non-zero -> nothing
- *             written.  GL_DEV_BAD_INDEX is ORed in for a given index outside
+ *   status    device int32 status word (required), read once as the call's
+ *             work begins: non-zero -> nothing written.  GL_DEV_BAD_INDEX is ORed in for a given index outside
  *             -1 .. E - 1 or an expert that a token has twice (y is then not
  *             written), GL_DEV_TIMEOUT for a wait that ran out (y incomplete).
  *   workspace device scratch of workspace_bytes >= gl_moe_workspace_bytes(T,

@@ -355,3 +355,40 @@ def test_weights_of_absent_choices_are_not_used(T):
         assert torch.equal(y, want) and int(st.item()) == 0
         if T > 1:
             assert not y[1].any()
+
+
+@pytest.mark.parametrize("T,given", [(3, False), (3, True), (40, False), (40, True)])
+def test_a_status_word_that_changes_meanwhile(T, given):
+    """Another stream sets and clears the status word while calls run: each call writes all of its outputs or none of
+    them, and none waits for CTAs that went by another value (such a wait takes two seconds)."""
+    E, k, H, F, n = 16, 4, 512, 256, 80
+    x, router, w1, w2 = _layer(T, E, H, F)
+    st, ws = _status(), torch.empty(gl.moe_workspace_bytes(T, E, k, H, F), dtype=torch.uint8, device="cuda")
+    want = gl.gl_moe_tokens(x, w1, w2, k, st, router_w=router, workspace=ws)
+    ys = [sentinel_like(T, H) for _ in range(n)]
+    if given:
+        routes = [dict(topk_idx=want[1], topk_w=want[2])] * n
+    else:
+        routes = [dict(router_w=router, topk_idx=torch.full((T, k), -7, dtype=torch.int32, device="cuda"),
+                       topk_w=torch.full((T, k), -7.0, device="cuda")) for _ in range(n)]
+    calls, setter = torch.cuda.Stream(), torch.cuda.Stream()
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    begin.record(calls)
+    for y, r in zip(ys, routes):
+        with torch.cuda.stream(calls):
+            gl.gl_moe_tokens(x, w1, w2, k, st, y=y, workspace=ws, **r)
+        with torch.cuda.stream(setter):
+            for _ in range(4):
+                st.fill_(gl.GL_DEV_NEG_SPLIT)
+                st.zero_()
+    end.record(calls)
+    torch.cuda.synchronize()
+    assert begin.elapsed_time(end) < 1500
+    for y, r in zip(ys, routes):
+        if untouched(y):
+            assert given or ((r["topk_idx"] == -7).all() and (r["topk_w"] == -7).all())
+        else:
+            assert torch.equal(y, want[0]) and torch.equal(r["topk_idx"], want[1]) and torch.equal(r["topk_w"], want[2])
+    st.zero_()
+    assert torch.equal(gl.gl_moe_tokens(x, w1, w2, k, st, workspace=ws, **routes[0])[0], want[0]) and int(st.item()) == 0
