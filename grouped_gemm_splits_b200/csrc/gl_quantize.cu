@@ -128,8 +128,10 @@ __global__ void __launch_bounds__(kQThreads + 32, QCfg<kCB>::kCtasPerSm)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + kStages);
   int64_t* bprefix = reinterpret_cast<int64_t*>(qsmem + kStages * Q::kTileBytes + 128);  // G+1 (ragged)
   int64_t* qprefix = bprefix + G + 1;                                                    // G+1 (ragged)
-  if (status != nullptr && *reinterpret_cast<volatile int32_t*>(status) != 0) return;
+  volatile int* skip_flag = abort_flag + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // one thread reads the status word for the CTA: a call beside this one may set it meanwhile
+  const int set = tid == 0 && status != nullptr ? *reinterpret_cast<volatile int32_t*>(status) : 0;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -166,7 +168,9 @@ __global__ void __launch_bounds__(kQThreads + 32, QCfg<kCB>::kCtasPerSm)
     }
     if (lane == 0) { bprefix[0] = 0; qprefix[0] = 0; }
   }
+  if (tid == 0) *skip_flag = set;
   __syncthreads();
+  if (*skip_flag != 0) return;
   if (kDbias && blockIdx.x == 0 && row_offsets != nullptr)
     for (int i = tid; i <= G; i += blockDim.x) part_prefix[i] = bprefix[i];
   const int64_t nblocks = (row_offsets != nullptr) ? bprefix[G] : bpg * G;
