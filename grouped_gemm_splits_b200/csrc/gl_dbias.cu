@@ -55,7 +55,7 @@ __global__ void __cluster_dims__(kDCluster, 1, 1) __launch_bounds__(kDThreads)
                  const int32_t* __restrict__ status, int N, int strips, __nv_bfloat16* __restrict__ out,
                  const __grid_constant__ DbiasPG pg, int per_group) {
   __shared__ __align__(16) float part[kDWarps][kDCols];
-  if (status != nullptr && *status != 0) return;  // every CTA of the cluster reads the same word
+  __shared__ int skip_s;
   const int unit = static_cast<int>(blockIdx.x) / kDCluster;
   const uint32_t crank = cluster_ctarank();
   const int g = unit / strips;
@@ -64,10 +64,15 @@ __global__ void __cluster_dims__(kDCluster, 1, 1) __launch_bounds__(kDThreads)
   const int col = strip * kDCols + lane * 4;  // this lane's 4 columns
   const bool col_ok = col < N;                // N % 8 == 0, so 4 columns are all in or all out
   const int64_t r0 = offsets[g], r1 = offsets[g + 1];
+  // One thread reads the status word for its CTA, and a CTA that finds it set
+  // stays and adds nothing: another call may set it meanwhile, and the cluster's
+  // CTAs read one another's shared memory.
+  if (threadIdx.x == 0) skip_s = status != nullptr && *reinterpret_cast<const volatile int32_t*>(status) != 0;
+  __syncthreads();
   constexpr int kStride = kDCluster * kDWarps;  // rows between a warp's consecutive rows
 
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (col_ok) {
+  if (col_ok && skip_s == 0) {
     const T* base = dy + col;
     int64_t r = r0 + static_cast<int>(crank) * kDWarps + warp;
     // kDUnroll independent rows per iteration keep loads in flight
@@ -103,14 +108,18 @@ __global__ void __cluster_dims__(kDCluster, 1, 1) __launch_bounds__(kDThreads)
   if (crank == 0 && threadIdx.x < kDCols) {
     const int c = strip * kDCols + static_cast<int>(threadIdx.x);
     float s = part[0][threadIdx.x];
+    int skip = skip_s;  // of any CTA: its rows are missing, nothing is written
     const uint32_t mine = smem_u32(&part[0][threadIdx.x]);
 #pragma unroll
     for (uint32_t k = 1; k < kDCluster; ++k) {
       float v;
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(mine, k)) : "memory");
       s += v;
+      int other;
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(other) : "r"(mapa_shared(smem_u32(&skip_s), k)) : "memory");
+      skip |= other;
     }
-    if (c < N) {
+    if (c < N && skip == 0) {
       __nv_bfloat16* dst = per_group ? pg.ptr[g] : out + static_cast<int64_t>(g) * N;
       dst[c] = __float2bfloat16_rn(s);
     }

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from grouped_gemm_splits_b200 import gl
-from tests.gpu_util import offsets_on_device
+from tests.gpu_util import SENTINEL_BF16, offsets_on_device, sentinel_like
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -59,3 +59,32 @@ def test_cast(ragged):
 
 def _bytes(rows, cols, G):
     return torch.full((gl.mxfp8_scale_bytes(rows, cols, G, True, True),), 0xA5, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_bias_gradient(fused):
+    """Column sums: a group's strip of 128 columns is written whole, from all of its rows, or not at all."""
+    rows, cols, G, n = 2048, 1024, 3, 100
+    dy = _rand(rows, cols)
+    off, st = offsets_on_device([700, 0, 1348], rows)
+    ws = torch.empty(gl.dbias_workspace_bytes(rows, cols, G), dtype=torch.uint8, device="cuda")
+    out = {}
+
+    def call(db):
+        if fused:
+            gl.group_quantize_mxfp8_dbias(dy, off, st, out=out, dbias=db, workspace=ws)
+        else:
+            gl.gl_dbias(dy, off, st, db)
+
+    want = sentinel_like(G, cols)
+    call(want)
+    outs = [sentinel_like(G, cols) for _ in range(n)]
+    assert _while_it_changes(st, [lambda o=o: call(o) for o in outs]) < 1500
+    for o in outs:
+        strips, right = o.view(G, cols // 128, 128), want.view(G, cols // 128, 128)
+        blank = (strips.view(torch.int16) == SENTINEL_BF16).all(2)
+        if not fused:  # (the fused call's sums may lack a cast that was held back)
+            assert (blank | (strips == right).all(2)).all()
+    st.zero_()
+    call(outs[0])
+    assert torch.equal(outs[0], want)
