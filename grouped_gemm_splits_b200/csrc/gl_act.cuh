@@ -7,7 +7,7 @@
 //          0.5 (1 + tanh v) = q(2v))
 // The gated forms act on pairs: swiglu silu(u0) * u1, geglu gelu(u0) * u1.
 //
-// e^x and the division are CUDA's fast forms (a few units in the last place
+// e^x and the reciprocal are the fast forms (a few units in the last place
 // of fp32, and results go to bf16).  A NaN stays a NaN in every value.
 #pragma once
 
@@ -24,7 +24,16 @@ __host__ __device__ constexpr int act_inner(int act) {
   return act == GL_ACT_SWIGLU ? GL_ACT_SILU : act == GL_ACT_GEGLU ? GL_ACT_GELU : act;
 }
 
-__device__ __forceinline__ float act_sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+// 1 / (1 + e^-v) from t = e^-|v| <= 1, which keeps the denominator in [1, 2]:
+// 1 / (1 + t), or t / (1 + t) below 0.  From 1 / (1 + e^-v) the fast division
+// gives 0 where its denominator is past 2^126, and e^-v overflows behind
+// -88.7, while silu stays in bf16's normal range down to -91.8.
+__device__ __forceinline__ float act_sigmoid(float v) {
+  const float t = __expf(-fabsf(v));
+  float r;  // of 1 .. 2: no subnormal on either side
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+  return v < 0.0f ? t * r : r;
+}
 
 constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
@@ -61,7 +70,9 @@ __device__ __forceinline__ float slope_of(float u, float& value) {
   if (ACT == GL_ACT_SILU) {
     const float q = act_sigmoid(u);
     value = u * q;
-    return q * fmaf(u, 1.0f - q, 1.0f);
+    float slope;  // 0 where q is below the normal range (it is under 2^-119 there)
+    asm("mul.ftz.f32 %0, %1, %2;" : "=f"(slope) : "f"(q), "f"(fmaf(u, 1.0f - q, 1.0f)));
+    return slope;
   }
   value = u;
   return 1.0f;

@@ -323,3 +323,52 @@ def test_more_than_two_to_the_31_elements():
     dz = gl.gl_dgrad_act(dy, w2, z, off, st, gl.GL_ACT_SWIGLU)
     assert orc.rel_frobenius(f64(dz[-last:]), blk.dgrad_act(f64(dy[-last:]), f64(w2), m, "swiglu", f64(z[-last:]))) <= 5e-3
     assert not dz[:last].any() and int(st.item()) == 0
+
+
+def _sigmoid(v):
+    return np.where(v < 0, np.exp(-np.abs(v)), 1.0) / (1 + np.exp(-np.abs(v)))
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "swiglu"])
+def test_far_negative_arguments(name):
+    """Values down to bf16's smallest: e^-88 is past 2^126, and e^-89 past fp32's largest value, but u e^u is not 0.
+
+    Half a bf16 step (2^-8 relative; 2^-134 below bf16's normal range); the exponential's argument, 97 at most, is off by
+    three fp32 roundings (3 * 97 * 2^-24 < 2^-15, relative in the value); its subnormal results by 2^-150, times |u|;
+    and the last two bits of the fast forms, 2^-20.
+    """
+    u = np.concatenate([np.arange(-97.0, -79.9, 0.5), [-20.0, -5.0, -0.5, 0.0, 3.0]])
+    if name == "gelu":
+        u = np.concatenate([np.arange(-10.5, -9.0, 0.0625), [-3.0, -0.5, 0.0, 3.0]])
+    n, K = len(u), 64
+    width = 64
+    x = torch.zeros(3, K, dtype=BF, device="cuda")
+    x[:, 0] = 1
+    gated = name == "swiglu"
+    w = torch.zeros(1, width * (2 if gated else 1), K, dtype=BF, device="cuda")
+    w[0, :n, 0] = torch.tensor(u, dtype=BF, device="cuda")
+    if gated:
+        w[0, width:, 0] = 1
+    u = f64(w)[0, :n, 0]
+    off, st = offsets_on_device([3], 3)
+    y, z = gl.gl_fwd_act(x, w, None, off, st, gl.ACTS[name], save_z=True)
+    assert np.array_equal(f64(z)[0, :n], u)
+    c = 2 * np.sqrt(2 / np.pi)
+    v, dv = (c * (u + 0.044715 * u ** 3), c * (1 + 3 * 0.044715 * u * u)) if name == "gelu" else (u, 1.0)
+    q = _sigmoid(v)
+    rel, least = 2.0 ** -8 + 2.0 ** -15 + 2.0 ** -20, 2.0 ** -134 + np.abs(u) * 2.0 ** -150
+    ref = u * q
+    assert np.all(np.abs(f64(y)[:, :n] - ref) <= rel * np.abs(ref) + least)
+    assert np.all(f64(y)[0, :n][(u < 0) & (ref < -2.0 ** -130)] < 0)
+    # slope q + u q (1 - q) v'(u): its two terms are off like the value; silu's is 0 where q is below 2^-126
+    eye = torch.eye(width, device="cuda").to(BF).view(1, width, width)
+    dz = f64(gl.gl_dgrad_act(torch.ones(3, width, dtype=BF, device="cuda"), eye, z, off, st, gl.ACTS[name]))
+    if gated:  # the other factor's gradient: the value
+        assert np.all(np.abs(dz[:, width:width + n] - ref) <= rel * np.abs(ref) + least)
+    dz = dz[:, :n]
+    qs = q if name == "gelu" else np.where(q < 2.0 ** -126, 0, q)
+    first, second = qs, u * qs * _sigmoid(-v) * dv
+    bound = 2.0 ** -8 * np.abs(first + second) + (rel - 2.0 ** -8) * (np.abs(first) + np.abs(second)) \
+        + 2.0 ** -134 + (1 + np.abs(u * dv)) * 2.0 ** -149
+    assert np.all(np.abs(dz - (first + second)) <= bound)
+    assert int(st.item()) == 0
