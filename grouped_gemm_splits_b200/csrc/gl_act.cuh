@@ -8,7 +8,8 @@
 // The gated forms act on pairs: swiglu silu(u0) * u1, geglu gelu(u0) * u1.
 //
 // e^x and the reciprocal are the fast forms (a few units in the last place
-// of fp32, and results go to bf16).  A NaN stays a NaN in every value.
+// of fp32, and results go to bf16).  A NaN stays a NaN in every value
+// and slope.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -53,7 +54,7 @@ template <int ACT>
 __device__ __forceinline__ float slope_of(float u, float& value) {
   if (ACT == GL_ACT_RELU) {
     value = u < 0.0f ? 0.0f : u;
-    return u > 0.0f ? 1.0f : 0.0f;
+    return u > 0.0f ? 1.0f : u <= 0.0f ? 0.0f : u;
   }
   if (ACT == GL_ACT_RELU2) {
     value = u < 0.0f ? 0.0f : u * u;

@@ -439,7 +439,7 @@ gl_status gl_fwd_act(const void* x, gl_grouped w, const gl_grouped* bias, const 
  *   dz       device bf16 [dz_rows, K] ([dz_rows, 2K]), dz_rows >= M; rows
  *            [M, dz_rows) are not written; not the same buffer as z or dy
  * relu's slope at 0 is 0, and so is silu's below -87.3 (it is under 2^-119
- * there).  Limits: those of gl_dgrad.
+ * there); a NaN in z makes its gradients NaN.  Limits: those of gl_dgrad.
  */
 gl_status gl_dgrad_act(const void* dy, gl_grouped w, const void* z, int act, const int64_t* offsets,
                        int32_t* status, int G, int64_t M, int N, int K, void* dz, int64_t dz_rows,

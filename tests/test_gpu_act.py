@@ -372,3 +372,20 @@ def test_far_negative_arguments(name):
         + 2.0 ** -134 + (1 + np.abs(u * dv)) * 2.0 ** -149
     assert np.all(np.abs(dz - (first + second)) <= bound)
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("name", blk.ACTS[1:])
+def test_a_nan_goes_through_every_gradient(name):
+    """A NaN pre-activation makes its own gradient NaN, whatever the activation, and no other one."""
+    M, K, N = 40, 64, 32
+    two = 2 if name in blk.GATED else 1
+    dy, w, z = _rand(M, N, seed=1), _rand(1, N, K, seed=2, std=0.3), _rand(M, two * K, seed=3)
+    z[5, 20] = z[39, 0] = float("nan")
+    off, st = offsets_on_device([M], M)
+    nan = np.zeros((M, two * K), dtype=bool)
+    nan[5, 20] = nan[39, 0] = True
+    if two == 2:  # the value is the other factor's slope
+        nan[5, K + 20] = nan[39, K] = True
+    for pair in (True, False):
+        assert np.array_equal(np.isnan(f64(gl.gl_dgrad_act(dy, w, z, off, st, gl.ACTS[name], pair=pair))), nan)
+    assert int(st.item()) == 0
