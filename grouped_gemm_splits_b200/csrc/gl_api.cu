@@ -10,16 +10,17 @@ namespace {
 using gl::GemmCall;
 
 // Per-call GEMM options (NULL = defaults: CTA pairs, the kernels' own 2 s
-// wait bound).  False for values the header does not define.
-bool read_opts(const gl_gemm_opts* o, int* cta_pair, uint64_t* wait_ns, int* hold_loads) {
-  *cta_pair = 1;
+// wait bound).  False for values the header does not define.  by_size: the call
+// can leave the tile shape to the library (cta_pair -1), and does by default.
+bool read_opts(const gl_gemm_opts* o, int* cta_pair, uint64_t* wait_ns, int* hold_loads, bool by_size = false) {
+  *cta_pair = by_size ? -1 : 1;
   *wait_ns = 0;  // 0: the kernel's default bound
   *hold_loads = 0;
   if (o == nullptr) return true;
-  if (o->tiles != GL_TILES_PAIR && o->tiles != GL_TILES_SINGLE) return false;
+  if (o->tiles != GL_TILES_PAIR && o->tiles != GL_TILES_SINGLE && !(by_size && o->tiles == GL_TILES_BY_SIZE)) return false;
   if (o->wait_limit_us > GL_WAIT_LIMIT_MAX_US) return false;
   if (o->flags & ~GL_OPT_HOLD_LOADS) return false;
-  *cta_pair = (o->tiles == GL_TILES_PAIR) ? 1 : 0;
+  *cta_pair = o->tiles == GL_TILES_BY_SIZE ? -1 : o->tiles == GL_TILES_PAIR ? 1 : 0;
   *wait_ns = static_cast<uint64_t>(o->wait_limit_us) * 1000u;
   *hold_loads = (o->flags & GL_OPT_HOLD_LOADS) ? 1 : 0;
   return true;
@@ -195,7 +196,7 @@ gl_status gl_fwd_act(const void* x, gl_grouped w, const gl_grouped* bias, const 
   if (st != GL_OK) return st;
   int pair = 1, hold = 0;
   uint64_t wait_ns = 0;
-  if (!read_opts(opts, &pair, &wait_ns, &hold)) return GL_ERR_INVALID;
+  if (!read_opts(opts, &pair, &wait_ns, &hold, true)) return GL_ERR_INVALID;
   if (act < GL_ACT_NONE || act > GL_ACT_GEGLU) return GL_ERR_INVALID;
   if ((x == nullptr && M > 0) || (y == nullptr && M > 0) || offsets == nullptr || status == nullptr)
     return GL_ERR_INVALID;
@@ -221,7 +222,7 @@ gl_status gl_fwd_act(const void* x, gl_grouped w, const gl_grouped* bias, const 
   c.M = M;
   c.N = N;
   c.K = K;
-  c.cta_pair = opts == nullptr ? -1 : pair;
+  c.cta_pair = pair;
   c.wait_ns = wait_ns;
   c.hold_loads = hold;
   c.stream = to_stream(stream);
@@ -239,7 +240,7 @@ gl_status gl_dgrad_act(const void* dy, gl_grouped w, const void* z, int act, con
   if (st != GL_OK) return st;
   int pair = 1, hold = 0;
   uint64_t wait_ns = 0;
-  if (!read_opts(opts, &pair, &wait_ns, &hold)) return GL_ERR_INVALID;
+  if (!read_opts(opts, &pair, &wait_ns, &hold, true)) return GL_ERR_INVALID;
   if (act <= GL_ACT_NONE || act > GL_ACT_GEGLU) return GL_ERR_INVALID;
   if (((dy == nullptr || z == nullptr || dz == nullptr) && M > 0) || offsets == nullptr || status == nullptr)
     return GL_ERR_INVALID;
@@ -261,7 +262,7 @@ gl_status gl_dgrad_act(const void* dy, gl_grouped w, const void* z, int act, con
   c.M = M;
   c.N = N;
   c.K = K;
-  c.cta_pair = opts == nullptr ? -1 : pair;
+  c.cta_pair = pair;
   c.wait_ns = wait_ns;
   c.hold_loads = hold;
   c.stream = to_stream(stream);

@@ -40,7 +40,7 @@ class GlGrouped(ctypes.Structure):
                 ("ptrs", ctypes.POINTER(ctypes.c_void_p))]
 
 
-GL_TILES_PAIR, GL_TILES_SINGLE = 0, 1
+GL_TILES_PAIR, GL_TILES_SINGLE, GL_TILES_BY_SIZE = 0, 1, 2
 
 
 GL_OPT_HOLD_LOADS = 1
@@ -161,7 +161,8 @@ def _opts_open(pair: Optional[bool], wait_limit_us: int, flags: int):
     """The same where None for ``pair`` leaves the tile shape to the library."""
     if pair is None and not wait_limit_us and not flags:
         return None
-    return ctypes.pointer(GlGemmOpts(GL_TILES_SINGLE if pair is False else GL_TILES_PAIR, wait_limit_us, flags))
+    tiles = GL_TILES_BY_SIZE if pair is None else GL_TILES_PAIR if pair else GL_TILES_SINGLE
+    return ctypes.pointer(GlGemmOpts(tiles, wait_limit_us, flags))
 
 
 def gl_offsets(m_splits: torch.Tensor, expect_rows: int, out_rows: Optional[int] = None,

@@ -86,15 +86,17 @@ int gl_version(void);
 const char* gl_status_string(gl_status s);
 
 /*
- * gl_gemm_opts -- per-call options of the six grouped GEMMs (gl_fwd,
- * gl_dgrad, gl_wgrad and their MXFP8 forms); pass NULL for the defaults.
+ * gl_gemm_opts -- per-call options of the grouped products (gl_fwd,
+ * gl_dgrad, gl_wgrad, their MXFP8 forms, gl_fwd_act, gl_dgrad_act) and of
+ * gl_moe_tokens; pass NULL for the defaults.
  * They belong to the one call: the library keeps no mode between calls, so
  * callers on different threads never change each other's kernels.
  *
  *   tiles          GL_TILES_PAIR (0, the default): 256 x 256 output tiles
  *                  on pairs of CTAs (tcgen05 cta_group::2, one CTA per SM).
  *                  GL_TILES_SINGLE: 128 x 256 tiles on single CTAs.  Results
- *                  agree within rounding.
+ *                  agree within rounding.  GL_TILES_BY_SIZE: the library's
+ *                  choice; only for gl_fwd_act and gl_dgrad_act.
  *   wait_limit_us  bound, in microseconds, on each wait of the kernel's
  *                  load -> MMA -> epilogue pipeline that finds its barrier not
  *                  yet complete; 0 = the default (2 s), at most
@@ -112,6 +114,7 @@ const char* gl_status_string(gl_status s);
  */
 #define GL_TILES_PAIR 0
 #define GL_TILES_SINGLE 1
+#define GL_TILES_BY_SIZE 2
 #define GL_WAIT_LIMIT_MAX_US 2000000u
 #define GL_OPT_HOLD_LOADS 1u
 typedef struct gl_gemm_opts {
@@ -401,8 +404,9 @@ gl_status gl_wgrad_mxfp8(const uint8_t* x_codes_c, const uint8_t* x_scales_c, co
  *
  *   x, w, bias, offsets, status   as for gl_fwd; w [N, K] of a gated
  *             activation holds the F rows of the activated factor first
- *   opts      as for gl_fwd, but NULL leaves the tile shape to the library,
- *             which chooses by M, G and the widths (short groups: single CTAs)
+ *   opts      as for gl_fwd, but NULL and GL_TILES_BY_SIZE leave the tile
+ *             shape to the library, which chooses by M, G and the widths
+ *             (short groups: single CTAs)
  *   residual  NULL or device bf16 [M, columns of y]
  *   act       GL_ACT_*
  *   z         NULL or device bf16 [M, N], written: u, which gl_dgrad_act of

@@ -1,4 +1,6 @@
 """What gl_fwd_act and gl_dgrad_act refuse, before any CUDA call (no GPU)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -81,3 +83,32 @@ def test_binding_names_the_weight_it_refuses(w):
         gl.gl_fwd_act(_z(4, 16), w, None, OFF, ST, gl.GL_ACT_SILU)
     with pytest.raises(gl.GlError, match="w must be"):
         gl.gl_dgrad_act(_z(4, 32), w, _z(4, 16), OFF, ST, gl.GL_ACT_SILU)
+
+
+def _opts(tiles, wait=0, flags=0):
+    return ctypes.pointer(gl.GlGemmOpts(tiles, wait, flags))
+
+
+@pytest.mark.parametrize("tiles", [gl.GL_TILES_PAIR, gl.GL_TILES_SINGLE, gl.GL_TILES_BY_SIZE])
+def test_tile_choices(tiles):
+    """The library's choice can be combined with a wait bound (no rows: the arguments are checked, nothing launched)."""
+    assert _f(M=0, rows=0, opts=_opts(tiles, 5000)) == gl.GL_OK
+    assert _d(M=0, rows=0, opts=_opts(tiles, 5000)) == gl.GL_OK
+    assert _f(M=0, rows=0, opts=_opts(3)) == gl.GL_ERR_INVALID
+    assert _d(M=0, rows=0, opts=_opts(-1)) == gl.GL_ERR_INVALID
+
+
+def test_calls_with_one_default_refuse_a_choice_by_size():
+    lib, o = gl.load(), _opts(gl.GL_TILES_BY_SIZE)
+    assert lib.gl_fwd(16, W, None, 16, 16, 2, 0, 32, 16, 16, 0, o, None) == gl.GL_ERR_INVALID
+    assert lib.gl_dgrad(16, W, 16, 16, 2, 0, 32, 16, 16, 0, o, None) == gl.GL_ERR_INVALID
+    assert lib.gl_wgrad(16, 16, 16, 16, 2, 0, 32, 16, W, 1, o, None) == gl.GL_ERR_INVALID
+    assert lib.gl_moe_tokens(None, 16, W, W, gl.GL_ACT_SWIGLU, 0, 0, 8, 2, 64, 32, None, None, None, 16, 256, 1 << 40, o,
+                             None) == gl.GL_ERR_INVALID
+
+
+@pytest.mark.parametrize("pair,tiles", [(None, gl.GL_TILES_BY_SIZE), (True, gl.GL_TILES_PAIR),
+                                        (False, gl.GL_TILES_SINGLE)])
+def test_binding_keeps_the_choice_beside_a_wait_bound(pair, tiles):
+    assert gl._opts_open(pair, 2000, 0).contents.tiles == tiles
+    assert gl._opts_open(pair, 0, gl.GL_OPT_HOLD_LOADS).contents.tiles == tiles
