@@ -578,7 +578,7 @@ namespace {
 gl_status check_moe_dims(int T, int E, int k, int H, int F) {
   if (T < 0 || E <= 0 || k <= 0 || k > E || H <= 0 || F <= 0) return GL_ERR_INVALID;
   if (T > GL_MOE_MAX_TOKENS || E > GL_MOE_MAX_EXPERTS || k > GL_MOE_MAX_TOP_K) return GL_ERR_UNSUPPORTED;
-  if (H % 8 != 0 || F % 8 != 0 || H > (1 << 20) || F > (1 << 20)) return GL_ERR_UNSUPPORTED;
+  if (H % 8 != 0 || F % 8 != 0 || H > GL_MOE_MAX_WIDTH || F > GL_MOE_MAX_WIDTH) return GL_ERR_UNSUPPORTED;
   return GL_OK;
 }
 
@@ -606,7 +606,7 @@ gl_status gl_moe_tokens(const void* x, const void* router, gl_grouped w1, gl_gro
   if ((w1.mode != GL_STACKED || w2.mode != GL_STACKED) && E > GL_MOE_MAX_PER_GROUP) return GL_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(router) || !aligned16(y) || !grouped_aligned(w1, E) || !grouped_aligned(w2, E) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) || (reinterpret_cast<uintptr_t>(topk_idx) & 3u) ||
-      (reinterpret_cast<uintptr_t>(topk_w) & 3u))
+      (reinterpret_cast<uintptr_t>(topk_w) & 3u) || (reinterpret_cast<uintptr_t>(status) & 3u))
     return GL_ERR_UNSUPPORTED;
   if (T == 0) return GL_OK;
   gl::MoeCall c{};

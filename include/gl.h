@@ -556,8 +556,10 @@ size_t gl_rmsnorm_bwd_workspace_bytes(int64_t rows, int cols);
  *             matter.  Calls that can overlap on the GPU need one each.
  *   opts      NULL or per-call options (tiles must be GL_TILES_PAIR, the default)
  * A token whose logits hold a NaN gets NaN weights and a NaN y.
- * Limits: H % 8 == 0, F % 8 == 0, E <= GL_MOE_MAX_EXPERTS
- * (GL_MOE_MAX_PER_GROUP when w1 or w2 is per group), top_k <= GL_MOE_MAX_TOP_K and <= E.  T == 0 does nothing.
+ * Limits: H % 8 == 0, F % 8 == 0, H and F <= GL_MOE_MAX_WIDTH, E <=
+ * GL_MOE_MAX_EXPERTS (GL_MOE_MAX_PER_GROUP when w1 or w2 is per group), top_k
+ * <= GL_MOE_MAX_TOP_K and <= E; x, router, y and the weights 16-byte aligned,
+ * topk_idx, topk_w and status by their element.  T == 0 does nothing.
  * Two launches, the second a cooperative one: it starts once every SM is free
  * for one of its blocks.
  */
@@ -565,6 +567,7 @@ size_t gl_rmsnorm_bwd_workspace_bytes(int64_t rows, int cols);
 #define GL_MOE_MAX_EXPERTS 256
 #define GL_MOE_MAX_PER_GROUP 120
 #define GL_MOE_MAX_TOP_K 16
+#define GL_MOE_MAX_WIDTH 1048576
 #define GL_MOE_RENORM 1
 gl_status gl_moe_tokens(const void* x, const void* router, gl_grouped w1, gl_grouped w2, int act, int flags,
                         int T, int E, int top_k, int H, int F, int32_t* topk_idx, float* topk_w, void* y,

@@ -99,3 +99,14 @@ def test_binding_refuses(make):
 def test_binding_names_what_it_refuses(w1, w2, ws, why):
     with pytest.raises(gl.GlError, match=why):
         gl.gl_moe_tokens(_z(2, 64), w1, w2, 2, ST, router_w=_z(4, 64), workspace=ws)
+
+
+@pytest.mark.parametrize("kw", [dict(H=(1 << 20) + 8), dict(F=(1 << 20) + 8), dict(st=18)])
+def test_wide_layers_and_a_status_word_off_its_boundary_are_unsupported(kw):
+    assert _m(**kw) == gl.GL_ERR_UNSUPPORTED
+
+
+def test_the_widest_layer_has_a_workspace():
+    f, n = gl.load().gl_moe_workspace_bytes, 1 << 20
+    assert f(128, 256, 16, n, n) > 128 * 16 * (4 * n + 2 * n)
+    assert f(1, 8, 2, n + 8, 64) == 0 and f(1, 8, 2, 64, n + 8) == 0
