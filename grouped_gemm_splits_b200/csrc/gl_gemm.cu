@@ -1015,12 +1015,16 @@ gl_status launch_cg(const GemmCall& c) {
 // pairs against singles, 64 groups of 2048 x 2816 swiglu: 32768 rows 385 / 396
 // us, 24576 314 / 327, 16384 252 / 234, 2048 154 / 125; 8 groups of 14336 x 4096:
 // 8192 rows 802 / 907, 4096 474 / 437, 1024 238 / 264, 512 231 / 170 (of ten
-// such points the rule missed one, by 11%).
+// such points the rule missed one, by 11%).  A single group's tiles are known:
+// 1 group of 7168 x 4096 swiglu, 1025 rows 76 / 52, 1300 rows 77 / 89; of
+// 14336 x 4096, 1025 rows 161 / 101; of 4096 x 14336, 513 rows 72 / 62, 700 rows 86 / 99
+// (75 such points, none missed; eleven were, by up to 59%, with their tiles rounded down).
 bool pairs_fit_better(const GemmCall& c) {
   const bool gated = act_gated(c.act);
   const int64_t cols = c.mode == kFwd ? (gated ? (c.N / 2 + 127) / 128 : (c.N + 255) / 256) : (c.K + 255) / 256;
   auto waves = [&](int64_t rows, int64_t units) {
-    const int64_t row_tiles = std::max<int64_t>(std::min<int64_t>(c.G, c.M), c.M / rows + c.G / 2);
+    const int64_t row_tiles = c.G == 1 ? (c.M + rows - 1) / rows
+                                       : std::max<int64_t>(std::min<int64_t>(c.G, c.M), c.M / rows + c.G / 2);
     return (row_tiles * cols + units - 1) / units;
   };
   const int64_t sms = std::max(2, num_sms());

@@ -389,3 +389,32 @@ def test_a_nan_goes_through_every_gradient(name):
     for pair in (True, False):
         assert np.array_equal(np.isnan(f64(gl.gl_dgrad_act(dy, w, z, off, st, gl.ACTS[name], pair=pair))), nan)
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("M,K,N,act", [(1025, 7168, 4096, gl.GL_ACT_SWIGLU), (1025, 14336, 4096, gl.GL_ACT_NONE)])
+def test_the_tile_shape_chosen_for_one_group(M, K, N, act):
+    """One group's tiles are known exactly: five rows of 256-row tiles do not fit a wave of pairs here, nine of 128-row
+    tiles fit one of single CTAs, and pairs take half as long again.  (Times in turn, medians; the choice may be off by
+    a quarter.)"""
+    x, w = _rand(M, K), _rand(1, N, K, seed=1, std=0.02)
+    off, st = offsets_on_device([M], M)
+    graphs = {}
+    for pair in (None, True, False):
+        gl.gl_fwd_act(x, w, None, off, st, act, pair=pair)
+        torch.cuda.synchronize()
+        graphs[pair] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[pair]):
+            for _ in range(10):
+                gl.gl_fwd_act(x, w, None, off, st, act, pair=pair)
+    times = {pair: [] for pair in graphs}
+    for _ in range(9):
+        for pair, graph in graphs.items():
+            begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            begin.record()
+            graph.replay()
+            end.record()
+            torch.cuda.synchronize()
+            times[pair].append(begin.elapsed_time(end))
+    took = {pair: sorted(t)[4] for pair, t in times.items()}
+    assert took[None] <= 1.25 * min(took[True], took[False]), took
+    assert int(st.item()) == 0
