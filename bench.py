@@ -50,17 +50,20 @@ OP_SAMPLES = 50  # per-op medians are taken over at least this many steps
 # of the CUDA sources the capture ran.  When the sources have changed since,
 # the figures describe other kernels: the line then reports traffic as null.
 MEASURED_TRAFFIC = {
-    "csrc_digest": "05899e12ae36d1bb",
+    "csrc_digest": "f70e378a36218ee9",
     # the second step of `bench.py --steps 2 --warmup 3` under ncu (one pass,
-    # gpu__time_duration / dram__bytes_read / dram__bytes_write per launch)
-    "bf16_g8": {"fwd": 1962336512, "dgrad": 3284737792, "wgrad": 5773288704,
-                "quant_x": 219350528, "quant_w": 1878191104, "quant_dy": 914407680,
-                "fwd_mx": 1007970816, "dgrad_mx": 1400205312, "wgrad_mx": 3673631232},
+    # gpu__time_duration / dram__bytes_read / dram__bytes_write per launch).  What
+    # fwd and dgrad read again depends on the GPU: captures of the same kernels on
+    # four of them gave fwd 1.83-2.17 GB and dgrad 2.82-3.28, the rest within 1.5%.
+    "bf16_g8": {"fwd": 2111429120, "dgrad": 3149569024, "wgrad": 5774681088,
+                "quant_x": 219269888, "quant_w": 1877679616, "quant_dy": 914585088,
+                "fwd_mx": 1012530688, "dgrad_mx": 1398916096, "wgrad_mx": 3673488896},
     # `bench.py --workload stacked_g128_ragged --steps 1 --warmup 1` under ncu
-    # (the timed step's kernels; the MXFP8 wgrad from the warm-up step)
-    "stacked_g128_ragged": {"fwd": 6857675008, "dgrad": 4629791488, "wgrad": 15535091456,
-                            "quant_x": 1891062784, "quant_w": 7906281216, "quant_dy": 493842944,
-                            "fwd_mx": 2874321152, "dgrad_mx": 2815959040, "wgrad_mx": 14829575680},
+    # (the timed step's kernels; the MXFP8 wgrad from the warm-up step).  On three
+    # GPUs: fwd 5.60-6.86 GB, fwd_mx 2.67-2.87, the rest within 1.5%.
+    "stacked_g128_ragged": {"fwd": 6087148544, "dgrad": 4627119360, "wgrad": 15683444736,
+                            "quant_x": 1890917888, "quant_w": 7894889728, "quant_dy": 496823040,
+                            "fwd_mx": 2801412352, "dgrad_mx": 2816950272, "wgrad_mx": 14950169856},
 }
 
 

@@ -478,9 +478,10 @@ gl_status gl_dgrad_act(const void* dy, gl_grouped w, const void* z, int act, con
  * Limits: cols % 8 == 0 (16-byte rows), cols % 32 == 0 with codes,
  * cols % 128 == 0 with GL_SCALES_MMA, cols <= GL_NORM_MAX_COLS; pointers
  * 16-byte aligned (codes 8, scales and rstd by their element).  A row whose
- * sum of squares overflows fp32 (none with |s| below 2^56) has rstd 0; a row that
- * holds a NaN or an infinity gives NaN where the formula does.  rows == 0 does
- * nothing.
+ * sum of squares overflows fp32 (none with |s| below 2^56) has rstd 0; squares
+ * of |s| below 2^-63 lose bits, which shows where eps does not outweigh them.
+ * A row that holds a NaN or an infinity gives NaN where the formula does.
+ * rows == 0 does nothing.
  */
 #define GL_NORM_MAX_COLS 16384
 gl_status gl_rmsnorm(const void* x, const void* residual, const void* gamma, float eps, int64_t rows,
